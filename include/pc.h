@@ -1,8 +1,9 @@
 /*
  * pc.h — C ABI of the MI355X (gfx950) hot path of tiled, ensemble 3D-genome
  * diffusion inference: guided DDIM reverse steps over batched 64-bead
- * distance maps, overlap-consistency projection of adjacent tiles, and
- * classical-MDS recovery of a point cloud per map.
+ * distance maps, overlap-consistency projection of adjacent tiles,
+ * classical-MDS recovery of a point cloud per map, and the attention
+ * operators of a denoiser that reads each region's conditioning.
  *
  * Method: "ParaChromo: a parallel inference framework for conditioned, tiled
  * 3D genome diffusion" (Electronics 15(13):2750), over the ChromoGen sampler
@@ -27,7 +28,8 @@
  *         u1 = ((r >> 8) + 1) 2^-24 in (0, 1] and u2 = (r >> 8) 2^-24 in [0, 1):
  *         sqrt(-2 ln u1) cos(2 pi u2), then sqrt(-2 ln u1) sin(2 pi u2).
  * Memory: every array argument marked "device" is device memory owned by the
- *         caller and must be 16-byte aligned; "host" arrays are host memory.
+ *         caller and must be 16-byte aligned unless its entry point says
+ *         otherwise; "host" arrays are host memory.
  *         The library allocates no device memory and keeps no state between
  *         calls (pc_ddim_sample holds its schedule in a host buffer for the
  *         length of the call; the one setting, pc_set_max_dispatch_items, is
@@ -281,6 +283,149 @@ PC_API pc_status pc_kabsch_stitch(const float *coords, const pc_layout *layout, 
  */
 PC_API pc_status pc_kabsch_stitch_proper(const float *coords, const pc_layout *layout, float *chain, float *residual,
                                          void *stream);
+
+/* Operators of a denoiser network ---------------------------------------- */
+
+/*
+ * A conditional denoiser reads each region's conditioning through attention:
+ * the tokens of a map (its 64 beads, say) query the encoder states of the
+ * map's region, which have a length of their own (sections 3.1 and 3.3: one
+ * embedding per region, reused over samples and guidance weights).  Tensors
+ * are [batch][len][heads][dim]: `dim` values of a head are contiguous, the
+ * other strides are free.  The maps of region r are batches r group ..
+ * (r + 1) group - 1 of the queries; keys and values are stored once per region.
+ *
+ * Strides are in elements.  Each is a multiple of 16 bytes and non-negative
+ * (the stride of an axis of one entry is not looked at); an input may have
+ * stride 0 over an axis it is broadcast along, an output may not.
+ */
+typedef int32_t pc_dtype;
+#define PC_F32 0
+#define PC_BF16 1
+#define PC_F16 2
+
+#define PC_MAX_HEAD_DIM 128
+
+typedef struct pc_strides {
+    int64_t batch, token, head;
+} pc_strides;
+
+typedef struct pc_attention {
+    pc_dtype dtype;    /* of q, k, v, out and their gradients                          */
+    int32_t n_kv;      /* encoder states (regions) >= 0                                */
+    int32_t group;     /* query batches per encoder state >= 0; n_kv group in all      */
+    int32_t len_q;     /* query tokens per batch >= 0                                  */
+    int32_t len_k;     /* encoder tokens, 0..2^30                                      */
+    int32_t heads;     /* query heads >= 1                                             */
+    int32_t heads_kv;  /* key and value heads, dividing heads: head h reads h / (heads / heads_kv) */
+    int32_t dim;       /* head size, a multiple of 8 in 8..PC_MAX_HEAD_DIM             */
+    float scale;       /* of the scores, finite and > 0 (1 / sqrt(dim) is usual)       */
+    pc_strides q, k, v, out;
+    pc_strides dout, dq, dk, dv; /* backward only                                      */
+} pc_attention;
+
+/*
+ * Bytes of workspace that pc_cross_attention (backward = 0) or
+ * pc_cross_attention_backward (1) needs for these sizes (host); 0 where none.
+ * Errors: those of the call itself that concern `a`.
+ */
+PC_API pc_status pc_cross_attention_workspace(const pc_attention *a, int32_t backward, int64_t *bytes);
+
+/*
+ * Cross attention: per query head and token, out = sum_k p_k v_k with
+ * p = softmax over the attended keys of scale q . k.  A key is attended if its
+ * index is below kv_len[region] and its key_mask is not 0.  A query without an
+ * attended key gives zeros and lse = -inf.  What keys and values hold at
+ * places that are not attended (NaN, too) has no influence.
+ * Scores, softmax statistics and sums are float32; the probabilities are
+ * rounded to the tensors' type for their product with v, the output once.
+ * The result is deterministic.
+ *   q          device [n_kv group][len_q][heads][dim].
+ *   k, v       device [n_kv][len_k][heads_kv][dim].
+ *   kv_len     device int32 [n_kv] or NULL (len_k); taken into 0..len_k.
+ *   key_mask   device uint8 [n_kv][len_k] or NULL (all 1).
+ *   out        device [n_kv group][len_q][heads][dim], written.
+ *   lse        device float [n_kv group][len_q][heads] or NULL, written: log sum exp of the scores.
+ *   workspace  device, 16-byte aligned, of workspace_bytes >= pc_cross_attention_workspace;
+ *              NULL where that is 0.  Its contents need not be kept.
+ * q, k, v, out, lse are 16-byte aligned, kv_len 4-byte.  out may not overlap an input.
+ * Errors: NULL pointers (of arrays that have elements); sizes, strides or
+ * alignment out of their ranges; 2^31 or more query rows or 2^31 workgroups; a workspace too small.
+ */
+PC_API pc_status pc_cross_attention(const pc_attention *a, const void *q, const void *k, const void *v,
+                                    const int32_t *kv_len, const uint8_t *key_mask, void *out, float *lse,
+                                    void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of pc_cross_attention: with dout the gradient of out,
+ *   dP = dout v^T, dS = P (dP - rowsum(dout out)),
+ *   dq = scale dS k, dk = scale dS^T q, dv = P^T dout,
+ * dk and dv summed over all query batches and heads that read the key head.
+ * Places that are not attended get zeros.  Deterministic: no atomic sums.
+ *   out, lse      of the forward call (lse is required here).
+ *   dout          device, as out.
+ *   dq, dk, dv    device, as q, k, v, written.  None may overlap another array of the call.
+ * Other arguments and errors as pc_cross_attention.
+ */
+PC_API pc_status pc_cross_attention_backward(const pc_attention *a, const void *q, const void *k, const void *v,
+                                             const void *out, const float *lse, const void *dout,
+                                             const int32_t *kv_len, const uint8_t *key_mask, void *dq, void *dk,
+                                             void *dv, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * One side (queries or keys) of pc_qk_norm_rope: [batch][len][heads][dim].
+ */
+typedef struct pc_norm_side {
+    int32_t batch, len, heads;   /* batch, len >= 0, heads >= 1                             */
+    const void *x;               /* device, read                                            */
+    void *y;                     /* device, forward: written; may be x (with x's strides)   */
+    const float *weight;         /* device float [dim] or NULL (ones)                       */
+    const int32_t *positions;    /* device int32 [batch or 1][len] or NULL (0 .. len - 1)   */
+    int64_t positions_stride;    /* elements between batches of positions, 0 if shared      */
+    const void *dy;              /* device, backward: read                                  */
+    void *dx;                    /* device, backward: written; may be dy (with its strides) */
+    float *dweight;              /* device float [dim], backward: written, or NULL          */
+    pc_strides sx, sy, sdy, sdx;
+} pc_norm_side;
+
+/*
+ * Root-mean-square norm of every head of the queries and the keys, with a
+ * weight per value, and the rotation of the head by its token's position, in
+ * one pass:
+ *   n = x weight / sqrt(mean(x^2) + eps); then, for the pairs (a, b) of the
+ *   first rot_dim values, (a cos t - b sin t, b cos t + a sin t) with
+ *   t = position freqs[i] for pair i; other values stay n.
+ * Pair i is values (i, i + rot_dim/2), or (2 i, 2 i + 1) if interleaved != 0.
+ * Angles are reduced exactly (64-bit fixed point) for every int32 position;
+ * sums and the rotation are float32, the result is rounded once.
+ *   q, k         host structs; either may be NULL (then it is left out).  Tile
+ *                k of a chain starts at bead k (64 - overlap): its positions.
+ *   dim          head size of both, a multiple of 8 in 8..PC_MAX_HEAD_DIM.
+ *   rot_dim      values rotated: 0, or a multiple of 16 up to dim.
+ *   freqs        host double [rot_dim/2]: radians per position, |f| <= 2 pi (NULL if rot_dim = 0).
+ * x, y, weight, dy, dx, dweight are 16-byte aligned, positions 4-byte.
+ * Errors: q and k both NULL; NULL x, y (forward) or dy, dx (backward) of a side
+ * with elements; sizes, strides, alignment or parameters out of their ranges;
+ * 2^31 or more tokens a side.
+ */
+PC_API pc_status pc_qk_norm_rope(const pc_norm_side *q, const pc_norm_side *k, pc_dtype dtype, int32_t dim,
+                                 int32_t rot_dim, const double *freqs, int32_t interleaved, float eps, void *stream);
+
+/*
+ * Bytes of workspace of pc_qk_norm_rope_backward for these sizes (host).
+ */
+PC_API pc_status pc_qk_norm_rope_workspace(const pc_norm_side *q, const pc_norm_side *k, pc_dtype dtype, int32_t dim,
+                                           int32_t rot_dim, int64_t *bytes);
+
+/*
+ * Gradients of pc_qk_norm_rope from x and dy: dx and, where dweight is given,
+ * dweight = sum over the side's batches, tokens and heads (float32, in a fixed
+ * order: deterministic).  Arguments and errors as pc_qk_norm_rope, workspace
+ * as pc_cross_attention.
+ */
+PC_API pc_status pc_qk_norm_rope_backward(const pc_norm_side *q, const pc_norm_side *k, pc_dtype dtype, int32_t dim,
+                                          int32_t rot_dim, const double *freqs, int32_t interleaved, float eps,
+                                          void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Diagnostics ----------------------------------------------------------- */
 

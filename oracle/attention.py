@@ -1,0 +1,115 @@
+"""Cross attention of queries to encoder states of another length, and its gradients, from the definition.
+
+Arrays are [batch, len, heads, dim] as the library takes them: ``group`` query batches read one encoder state, and
+``heads / heads_kv`` query heads one key head.  ``keep`` [n_kv, len_k] marks the attended keys; a query without one has
+out = 0 and lse = -inf, and passes no gradient.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+
+
+def _per_query(x, B, H):
+    """Keys or values [R, Lk, Hk, D] repeated to [B, H, Lk, D]."""
+    R, _, Hk, _ = x.shape
+    x = np.repeat(np.repeat(x, B // R, axis=0), H // Hk, axis=2)
+    return x.transpose(0, 2, 1, 3)
+
+
+def _summed(x, R, Hk):
+    """[B, H, Lk, D] summed over the query batches and heads that share a key head: [R, Lk, Hk, D]."""
+    B, H, Lk, D = x.shape
+    return x.reshape(R, B // R, Hk, H // Hk, Lk, D).sum(axis=(1, 3)).transpose(0, 2, 1, 3)
+
+
+def attended(n_kv, len_k, kv_len=None, key_mask=None):
+    keep = np.ones((n_kv, len_k), dtype=bool)
+    if kv_len is not None:
+        keep &= np.arange(len_k)[None, :] < np.asarray(kv_len)[:, None]
+    if key_mask is not None:
+        keep &= np.asarray(key_mask) != 0
+    return keep
+
+
+def probabilities(q, k, keep, scale):
+    """(scores [B, H, Lq, Lk], P, lse [B, H, Lq])."""
+    B, _, H, _ = q.shape
+    qh = q.transpose(0, 2, 1, 3)
+    kh = np.where(np.repeat(keep, B // max(k.shape[0], 1), axis=0)[:, None, :, None], _per_query(k, B, H), 0.0)
+    s = scale * (qh @ kh.transpose(0, 1, 3, 2))
+    on = np.broadcast_to(np.repeat(keep, B // max(k.shape[0], 1), axis=0)[:, None, None, :], s.shape)
+    top = np.where(on, s, -np.inf).max(axis=-1, initial=-np.inf, keepdims=True)
+    top0 = np.where(np.isfinite(top), top, 0.0)
+    e = np.where(on, np.exp(np.where(on, s, 0.0) - top0), 0.0)
+    total = e.sum(axis=-1, keepdims=True)
+    with np.errstate(divide="ignore"):
+        lse = (top0 + np.log(total))[..., 0]
+    return s, e / np.where(total == 0.0, 1.0, total), lse
+
+
+def _clean(x, keep):
+    return np.where(keep[:, :, None, None], x, 0.0)
+
+
+def forward(q, k, v, keep, scale):
+    """(out [B, Lq, H, D], lse [B, Lq, H])."""
+    B, _, H, _ = q.shape
+    k, v = _clean(k, keep), _clean(v, keep)
+    _, p, lse = probabilities(q, k, keep, scale)
+    return (p @ _per_query(v, B, H)).transpose(0, 2, 1, 3), lse.transpose(0, 2, 1)
+
+
+def backward(q, k, v, dout, keep, scale):
+    """(dq, dk, dv)."""
+    B, _, H, _ = q.shape
+    R, _, Hk, _ = k.shape
+    k, v = _clean(k, keep), _clean(v, keep)
+    _, p, _ = probabilities(q, k, keep, scale)
+    qh, gh = q.transpose(0, 2, 1, 3), dout.transpose(0, 2, 1, 3)
+    kh, vh = _per_query(k, B, H), _per_query(v, B, H)
+    dp = gh @ vh.transpose(0, 1, 3, 2)
+    ds = scale * p * (dp - (p * dp).sum(axis=-1, keepdims=True))
+    dq = (ds @ kh).transpose(0, 2, 1, 3)
+    return dq, _summed(ds.transpose(0, 1, 3, 2) @ qh, R, Hk), _summed(p.transpose(0, 1, 3, 2) @ gh, R, Hk)
+
+
+def error_bounds(q, k, v, dout, keep, scale, u_out, u_p, abs_p, n_extra=64):
+    """Largest elementwise errors of (out, dq, dk, dv) of an evaluation that holds scores, statistics and sums in
+    float32, rounds P and dS to relative u_p for their products and results to u_out; below the type's normal range
+    both are rounded to absolute abs_p.
+
+    A score has error at most (D + 2) 2^-24 scale sum |q k|, the rounded exponent 4 |s| 2^-24; a sum over n terms adds
+    n 2^-24 of its absolute terms.  Probabilities below 2^-126 may be 0.  delta = sum dout out uses the rounded out.
+    """
+    f = 2.0 ** -24
+    B, Lq, H, D = q.shape
+    R, Lk, Hk, _ = k.shape
+    k, v = _clean(k, keep), _clean(v, keep)
+    s, p, _ = probabilities(q, k, keep, scale)
+    qh, gh = q.transpose(0, 2, 1, 3), dout.transpose(0, 2, 1, 3)
+    kh, vh = _per_query(k, B, H), _per_query(v, B, H)
+    sabs = scale * (np.abs(qh) @ np.abs(kh).transpose(0, 1, 3, 2))
+    # relative error of a probability of the row
+    e = f * (2 * (D + 2) * sabs.max(axis=-1, initial=0.0) + 8 * np.abs(s).max(axis=-1, initial=0.0) + Lk + n_extra)
+    e = e[..., None]
+    on = p > 0
+    pv, vabs = p @ np.abs(vh), on @ np.abs(vh)
+    o = p @ vh
+    t_out = u_out * np.abs(o) + (u_p + e) * pv + abs_p * vabs
+    dp = gh @ vh.transpose(0, 1, 3, 2)
+    delta = (p * dp).sum(axis=-1, keepdims=True)
+    t_delta = (np.abs(gh) * (t_out + D * f * np.abs(o))).sum(axis=-1, keepdims=True)
+    t_dp = D * f * (np.abs(gh) @ np.abs(vh).transpose(0, 1, 3, 2))
+    ds = p * (dp - delta)
+    t_ds = p * (e * np.abs(dp - delta) + t_dp + t_delta + 2 * f * (np.abs(dp) + np.abs(delta))) + u_p * np.abs(ds) \
+        + (abs_p + 2.0 ** -126 * np.abs(dp - delta)) * on
+    rows = (B // max(R, 1)) * Lq * (H // Hk)
+    t_dq = scale * (t_ds @ np.abs(kh)) + f * (Lk + n_extra) * scale * (np.abs(ds) @ np.abs(kh))
+    t_dk = scale * (t_ds.transpose(0, 1, 3, 2) @ np.abs(qh) + f * (rows + n_extra) * (
+        np.abs(ds).transpose(0, 1, 3, 2) @ np.abs(qh)))
+    t_dv = ((u_p + e + f * (rows + n_extra)) * p + abs_p * on).transpose(0, 1, 3, 2) @ np.abs(gh)
+    dq, dk, dv = backward(q, k, v, dout, keep, scale)
+    back = lambda x: x.transpose(0, 2, 1, 3)  # noqa: E731
+    return (back(t_out) + abs_p, back(t_dq) + u_out * np.abs(dq) + abs_p,
+            _summed(t_dk, R, Hk) + u_out * np.abs(dk) + abs_p, _summed(t_dv, R, Hk) + u_out * np.abs(dv) + abs_p)

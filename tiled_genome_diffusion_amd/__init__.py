@@ -17,7 +17,9 @@ from . import _lib
 
 __all__ = ["PCError", "PCLayout", "PACKED", "BEADS", "pc_version", "pc_last_error", "pc_ddim_schedule",
            "pc_ddim_schedule_cosine", "pc_init_state", "pc_ddim_cfg_step", "pc_ddim_cfg_step_eps", "pc_ddim_sample", "pc_seam_project", "pc_seam_discrepancy",
-           "pc_seam_mean_abs", "pc_mds_recover", "pc_kabsch_stitch", "pc_kabsch_stitch_proper", "pc_set_max_dispatch_items", "pc_philox_block", "pc_philox_fill", "pc_normal_fill", "pc_seam_index_map"]
+           "pc_seam_mean_abs", "pc_mds_recover", "pc_kabsch_stitch", "pc_kabsch_stitch_proper",
+           "pc_cross_attention", "pc_cross_attention_backward", "pc_cross_attention_workspace", "pc_qk_norm_rope",
+           "pc_qk_norm_rope_backward", "pc_qk_norm_rope_workspace", "pc_set_max_dispatch_items", "pc_philox_block", "pc_philox_fill", "pc_normal_fill", "pc_seam_index_map"]
 
 BEADS = 64
 PACKED = 2016
@@ -217,6 +219,240 @@ def pc_kabsch_stitch(coords, layout: PCLayout, chain, residual) -> None:
 def pc_kabsch_stitch_proper(coords, layout: PCLayout, chain, residual) -> None:
     """pc_kabsch_stitch with every fit restricted to rotations (det +1)."""
     _stitch("pc_kabsch_stitch_proper", coords, layout, chain, residual)
+
+
+_DTYPES: dict = {}
+
+
+def _dtype(t, name: str) -> int:
+    """The ABI's number of a tensor's element type."""
+    if not _DTYPES:
+        m = _torch()
+        _DTYPES.update({m.float32: 0, m.bfloat16: 1, m.float16: 2})
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return d
+
+
+def _like(t, name: str, shape, ref):
+    """Device pointer of a [batch, len, heads, dim] tensor on ref's device and of its type; heads are contiguous."""
+    if not t.is_cuda or t.device != ref.device:
+        raise ValueError(f"{name} must be a device tensor on {ref.device}")
+    if t.dtype != ref.dtype:
+        raise ValueError(f"{name} must be {ref.dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    return t.data_ptr()
+
+
+def _heads_of(t, name: str):
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [batch, len, heads, dim], got {tuple(t.shape)}")
+    return t.shape
+
+
+def _flat(t, name: str, dtype, shape, ref):
+    """Device pointer of a contiguous tensor of the given type and shape on ref's device, or None."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device != ref.device:
+        raise ValueError(f"{name} must be a device tensor on {ref.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _enqueue(ref, func, *args):
+    """func(*args, stream) on ref's device and torch's current stream there."""
+    cuda = _torch().cuda
+    if cuda.current_device() == ref.device.index:
+        return func(*args, cuda.current_stream().cuda_stream)
+    with cuda.device(ref.device):
+        return func(*args, cuda.current_stream().cuda_stream)
+
+
+def _workspace(given, need: int, ref):
+    """(pointer, bytes, owner) of a workspace: the caller's, or one from torch's allocator on the current stream."""
+    if given is None:
+        if need == 0:
+            return None, 0, None
+        given = _torch().empty(need, dtype=_torch().uint8, device=ref.device)
+    elif not given.is_cuda or given.device != ref.device or not given.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {ref.device}")
+    return given.data_ptr(), given.numel() * given.element_size(), given
+
+
+def _attention(q, k, v, scale):
+    (B, Lq, H, D), (R, Lk, Hk, Dk) = _heads_of(q, "q"), _heads_of(k, "k")
+    if Dk != D:
+        raise ValueError(f"q has heads of {D} values, k of {Dk}")
+    if (B % R != 0) if R else B:
+        raise ValueError(f"{R} encoder states must divide {B} query batches")
+    a = _lib.Attention(_dtype(q, "q"), R, B // R if R else 0, Lq, Lk, H, Hk, D, D ** -0.5 if scale is None else scale)
+    a.q, a.k, a.v = q.stride()[:3], k.stride()[:3], v.stride()[:3]
+    return a
+
+
+def pc_cross_attention_workspace(q, k, v, backward: bool = False, scale=None) -> int:
+    """Bytes of workspace of pc_cross_attention (or its backward) for these tensors."""
+    a = _attention(q, k, v, scale)
+    a.out = q.stride()[:3]
+    if backward:
+        a.dout, a.dq, a.dk, a.dv = a.q, a.q, a.k, a.v
+    n = ctypes.c_int64()
+    _check(_lib.load().pc_cross_attention_workspace(ctypes.addressof(a), int(backward), ctypes.addressof(n)),
+           "pc_cross_attention_workspace")
+    return n.value
+
+
+def pc_cross_attention(q, k, v, out, lse=None, kv_len=None, key_mask=None, scale=None, workspace=None) -> None:
+    """out = softmax(scale q k^T) v per head: q, out [n_kv * group, len_q, heads, dim]; k, v [n_kv, len_k, heads_kv, dim].
+
+    lse float32 [n_kv * group, len_q, heads]; kv_len int32 [n_kv]; key_mask uint8 or bool [n_kv, len_k]; scale defaults
+    to dim ** -0.5.  Without a workspace one is taken from torch's allocator where it is needed."""
+    t = _torch()
+    lib = _lib.load()
+    a = _attention(q, k, v, scale)
+    R, Lk = k.shape[0], k.shape[1]
+    ptrs = (_like(q, "q", q.shape, q), _like(k, "k", k.shape, q), _like(v, "v", k.shape, q),
+            _flat(kv_len, "kv_len", t.int32, (R,), q),
+            _flat(key_mask.view(t.uint8) if key_mask is not None and key_mask.dtype == t.bool else key_mask, "key_mask",
+                  t.uint8, (R, Lk), q),
+            _like(out, "out", q.shape, q), _flat(lse, "lse", t.float32, q.shape[:3], q))
+    a.out = out.stride()[:3]
+    n = ctypes.c_int64()
+    _check(lib.pc_cross_attention_workspace(ctypes.addressof(a), 0, ctypes.addressof(n)), "pc_cross_attention")
+    p, size, keep = _workspace(workspace, n.value, q)
+    _check(_enqueue(q, lib.pc_cross_attention, ctypes.addressof(a), *ptrs, p, size), "pc_cross_attention")
+
+
+def pc_cross_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, kv_len=None, key_mask=None, scale=None,
+                                workspace=None) -> None:
+    """dq, dk, dv of pc_cross_attention from its inputs, out, lse and dout (arguments as there)."""
+    t = _torch()
+    lib = _lib.load()
+    a = _attention(q, k, v, scale)
+    R, Lk = k.shape[0], k.shape[1]
+    if lse is None:
+        raise ValueError("lse of the forward call is required")
+    first = (_like(q, "q", q.shape, q), _like(k, "k", k.shape, q), _like(v, "v", k.shape, q),
+             _like(out, "out", q.shape, q), _flat(lse, "lse", t.float32, q.shape[:3], q),
+             _like(dout, "dout", q.shape, q), _flat(kv_len, "kv_len", t.int32, (R,), q),
+             _flat(key_mask.view(t.uint8) if key_mask is not None and key_mask.dtype == t.bool else key_mask,
+                   "key_mask", t.uint8, (R, Lk), q),
+             _like(dq, "dq", q.shape, q), _like(dk, "dk", k.shape, q), _like(dv, "dv", k.shape, q))
+    a.out, a.dout = out.stride()[:3], dout.stride()[:3]
+    a.dq, a.dk, a.dv = dq.stride()[:3], dk.stride()[:3], dv.stride()[:3]
+    n = ctypes.c_int64()
+    _check(lib.pc_cross_attention_workspace(ctypes.addressof(a), 1, ctypes.addressof(n)),
+           "pc_cross_attention_backward")
+    p, size, keep = _workspace(workspace, n.value, q)
+    _check(_enqueue(q, lib.pc_cross_attention_backward, ctypes.addressof(a), *first, p, size),
+           "pc_cross_attention_backward")
+
+
+def _norm_side(x, weight, positions, ref, name: str):
+    t = _torch()
+    B, L, H, D = _heads_of(x, name)
+    s = _lib.NormSide(B, L, H, _like(x, name, x.shape, ref))
+    s.weight = _flat(weight, name + "_weight", t.float32, (D,), ref)
+    s.sx = x.stride()[:3]
+    if positions is not None:
+        if not positions.is_cuda or positions.device != ref.device or positions.dtype != t.int32:
+            raise ValueError(f"{name}_positions must be int32 on {ref.device}")
+        if tuple(positions.shape) not in ((L,), (1, L), (B, L)) or (L > 1 and positions.stride(-1) != 1):
+            raise ValueError(f"{name}_positions must be [{L}] or [{B}, {L}] with contiguous rows, "
+                             f"got {tuple(positions.shape)}")
+        s.positions = positions.data_ptr()
+        s.positions_stride = positions.stride(0) if positions.dim() == 2 and positions.shape[0] > 1 else 0
+    return s
+
+
+def _freqs(freqs):
+    f = np.ascontiguousarray(freqs, dtype=np.float64).reshape(-1)
+    return f, f.ctypes.data if f.size else None
+
+
+def _norm_ref(q, k):
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q and k are both None")
+    _heads_of(ref, "q" if q is not None else "k")
+    if q is not None and k is not None and _heads_of(k, "k")[3] != q.shape[3]:
+        raise ValueError(f"q has heads of {q.shape[3]} values, k of {k.shape[3]}")
+    return ref
+
+
+def pc_qk_norm_rope(q, k, q_weight, k_weight, q_positions, k_positions, freqs, q_out, k_out, eps: float = 1e-6,
+                    interleaved: bool = False) -> None:
+    """Root-mean-square norm per head of q and k [batch, len, heads, dim] and the rotation of their first
+    2 len(freqs) values by position, into q_out and k_out (which may be q and k).
+
+    Weights float32 [dim] or None; positions int32 [batch, len] or [len], or None for 0 .. len - 1; freqs radians per
+    position of each pair (float64, host).  q or k may be None, with its other arguments."""
+    lib = _lib.load()
+    ref = _norm_ref(q, k)
+    sides = []
+    for x, w, pos, out, name in ((q, q_weight, q_positions, q_out, "q"), (k, k_weight, k_positions, k_out, "k")):
+        s = None
+        if x is not None:
+            s = _norm_side(x, w, pos, ref, name)
+            s.y, s.sy = _like(out, name + "_out", x.shape, ref), out.stride()[:3]
+        sides.append(s)
+    f, fp = _freqs(freqs)
+    p = [None if s is None else ctypes.addressof(s) for s in sides]
+    _check(_enqueue(ref, lib.pc_qk_norm_rope, *p, _dtype(ref, "q"), ref.shape[3], 2 * f.size, fp, int(bool(interleaved)),
+                    float(eps)), "pc_qk_norm_rope")
+
+
+def pc_qk_norm_rope_workspace(q, k, freqs) -> int:
+    """Bytes of workspace of pc_qk_norm_rope_backward for these tensors."""
+    ref = _norm_ref(q, k)
+    sides = []
+    for x, name in ((q, "q"), (k, "k")):
+        s = None
+        if x is not None:
+            s = _norm_side(x, None, None, ref, name)
+            s.sdy = s.sdx = s.sx
+        sides.append(s)
+    n = ctypes.c_int64()
+    p = [None if s is None else ctypes.addressof(s) for s in sides]
+    _check(_lib.load().pc_qk_norm_rope_workspace(*p, _dtype(ref, "q"), ref.shape[3], 2 * len(freqs),
+                                                 ctypes.addressof(n)), "pc_qk_norm_rope_workspace")
+    return n.value
+
+
+def pc_qk_norm_rope_backward(q, k, q_weight, k_weight, q_positions, k_positions, freqs, dq_out, dk_out, dq, dk,
+                             dq_weight=None, dk_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                             workspace=None) -> None:
+    """Gradients of pc_qk_norm_rope: dq, dk (which may be dq_out, dk_out) and, where given, dq_weight and dk_weight."""
+    t = _torch()
+    lib = _lib.load()
+    ref = _norm_ref(q, k)
+    sides = []
+    for x, w, pos, dy, dx, dw, name in ((q, q_weight, q_positions, dq_out, dq, dq_weight, "q"),
+                                        (k, k_weight, k_positions, dk_out, dk, dk_weight, "k")):
+        s = None
+        if x is not None:
+            s = _norm_side(x, w, pos, ref, name)
+            s.dy, s.sdy = _like(dy, f"d{name}_out", x.shape, ref), dy.stride()[:3]
+            s.dx, s.sdx = _like(dx, f"d{name}", x.shape, ref), dx.stride()[:3]
+            s.dweight = _flat(dw, f"d{name}_weight", t.float32, (x.shape[3],), ref)
+        sides.append(s)
+    f, fp = _freqs(freqs)
+    p = [None if s is None else ctypes.addressof(s) for s in sides]
+    D = ref.shape[3]
+    n = ctypes.c_int64()
+    _check(lib.pc_qk_norm_rope_workspace(*p, _dtype(ref, "q"), D, 2 * f.size, ctypes.addressof(n)),
+           "pc_qk_norm_rope_backward")
+    wp, size, keep = _workspace(workspace, n.value, ref)
+    _check(_enqueue(ref, lib.pc_qk_norm_rope_backward, *p, _dtype(ref, "q"), D, 2 * f.size, fp, int(bool(interleaved)),
+                    float(eps), wp, size), "pc_qk_norm_rope_backward")
 
 
 def pc_set_max_dispatch_items(items: int) -> None:

@@ -21,6 +21,25 @@ class Layout(ctypes.Structure):
                 ("chain_len", ctypes.c_int32), ("overlap", ctypes.c_int32)]
 
 
+class Strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class Attention(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("len_q", ctypes.c_int32), ("len_k", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("heads_kv", ctypes.c_int32), ("dim", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", Strides), ("k", Strides), ("v", Strides), ("out", Strides),
+                ("dout", Strides), ("dq", Strides), ("dk", Strides), ("dv", Strides)]
+
+
+class NormSide(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("len", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("x", vp), ("y", vp), ("weight", vp), ("positions", vp), ("positions_stride", ctypes.c_int64),
+                ("dy", vp), ("dx", vp), ("dweight", vp),
+                ("sx", Strides), ("sy", Strides), ("sdy", Strides), ("sdx", Strides)]
+
+
 # name -> (restype, argtypes), in the order of include/pc.h
 SIGNATURES = {
     "pc_version": (ctypes.c_char_p, []),
@@ -46,6 +65,15 @@ SIGNATURES = {
     "pc_mds_recover": (ctypes.c_int32, [vp, ctypes.c_int64, vp, vp, ctypes.c_int32, vp]),
     "pc_kabsch_stitch": (ctypes.c_int32, [vp, ctypes.POINTER(Layout), vp, vp, vp]),
     "pc_kabsch_stitch_proper": (ctypes.c_int32, [vp, ctypes.POINTER(Layout), vp, vp, vp]),
+    "pc_cross_attention_workspace": (ctypes.c_int32, [vp, ctypes.c_int32, vp]),
+    "pc_cross_attention": (ctypes.c_int32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp]),
+    "pc_cross_attention_backward": (ctypes.c_int32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                     ctypes.c_int64, vp]),
+    "pc_qk_norm_rope": (ctypes.c_int32, [vp, vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, ctypes.c_int32,
+                                         ctypes.c_float, vp]),
+    "pc_qk_norm_rope_workspace": (ctypes.c_int32, [vp, vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp]),
+    "pc_qk_norm_rope_backward": (ctypes.c_int32, [vp, vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp,
+                                                  ctypes.c_int32, ctypes.c_float, vp, ctypes.c_int64, vp]),
     "pc_set_max_dispatch_items": (ctypes.c_int32, [ctypes.c_uint64]),
     "pc_philox_block": (ctypes.c_int32, [c_u32_p, c_u32_p, ctypes.c_uint64]),
     "pc_philox_fill": (ctypes.c_int32, [vp, ctypes.POINTER(Layout), ctypes.c_uint64, ctypes.c_uint32, vp]),

@@ -19,7 +19,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpc.so")
-SOURCES = ["api.hip", "step.hip", "chain.hip", "seam.hip", "mds.hip", "stitch.hip"]
+SOURCES = ["api.hip", "step.hip", "chain.hip", "seam.hip", "mds.hip", "stitch.hip", "api_attn.hip", "attn_fwd.hip",
+           "attn_bwd.hip", "norm_rope.hip"]
 CEILING_LIB = os.path.join(HERE, "libpc_ceiling.so")
 CEILING_SOURCES = ["ceiling.hip"]
 ARCH = "gfx950"

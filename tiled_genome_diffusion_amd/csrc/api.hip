@@ -11,13 +11,15 @@
 #include "pc.h"
 #include "common.hpp"
 #include "launch.hpp"
+#include "status.hpp"
 
 namespace {
 
 thread_local char g_err[256] = "";
 
-pc_status fail(pc_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
-pc_status fail(pc_status st, const char *fmt, ...) {
+}  // namespace
+
+pc_status pc::fail(pc_status st, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(g_err, sizeof g_err, fmt, ap);
@@ -25,17 +27,22 @@ pc_status fail(pc_status st, const char *fmt, ...) {
     return st;
 }
 
-pc_status ok() {
+pc_status pc::ok() {
     g_err[0] = '\0';
     return PC_OK;
 }
 
-pc_status hip_status(hipError_t e, const char *what) {
+pc_status pc::hip_status(hipError_t e, const char *what) {
     if (e == hipSuccess) return ok();
     return fail(PC_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
+
+using pc::aligned16;
+using pc::fail;
+using pc::hip_status;
+using pc::ok;
 
 // Validates a layout; on success stores the map count.
 pc_status check_layout(const pc_layout *L, int64_t *n_maps) {

@@ -1,0 +1,325 @@
+// C ABI of the denoiser operators (include/pc.h): argument validation and
+// launches of cross attention and of the norm of queries and keys with the
+// position rotation.
+#include <math.h>
+#include <string.h>
+
+#include "attn.hpp"
+#include "norm_rope.hpp"
+#include "pc.h"
+#include "status.hpp"
+
+namespace {
+
+using pc::aligned16;
+using pc::fail;
+using pc::hip_status;
+using pc::ok;
+
+static_assert(PC_F32 == pc::kF32 && PC_BF16 == pc::kBf16 && PC_F16 == pc::kF16, "element type numbers");
+static_assert(sizeof(pc::NormArgs) + 8 <= 4096 && sizeof(pc::AttnArgs) + 8 <= 4096, "kernel arguments");
+
+bool same(const pc::HeadStrides &x, const pc::HeadStrides &y) { return x.b == y.b && x.t == y.t && x.h == y.h; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+pc_status check_dtype_dim(pc_dtype dtype, int32_t dim) {
+    if (dtype != PC_F32 && dtype != PC_BF16 && dtype != PC_F16) return fail(PC_ERR_PARAM, "unknown dtype %d", dtype);
+    if (dim < 8 || dim > PC_MAX_HEAD_DIM || dim % 8 != 0)
+        return fail(PC_ERR_SHAPE, "head size %d is not a multiple of 8 in 8..%d", dim, PC_MAX_HEAD_DIM);
+    return PC_OK;
+}
+
+// Strides of [batch][len][heads][dim] and the reach of the last element, in
+// range; on success stores the strides with those of single-entry axes zeroed.
+pc_status check_strides(const char *name, const pc_strides &s, pc_dtype dtype, int64_t batch, int64_t len,
+                        int64_t heads, int32_t dim, bool output, pc::HeadStrides *out) {
+    const int64_t unit = dtype == PC_F32 ? 4 : 8;
+    const int64_t stride[3] = {s.batch, s.token, s.head}, n[3] = {batch, len, heads};
+    int64_t kept[3] = {0, 0, 0};
+    int64_t reach = dim;
+    bool empty = false;
+    for (int i = 0; i < 3; ++i) empty = empty || n[i] == 0;
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] <= 1 || empty) continue;
+        if (stride[i] < 0 || stride[i] % unit != 0)
+            return fail(PC_ERR_SHAPE, "%s: stride %lld is negative or not a multiple of 16 bytes", name,
+                        static_cast<long long>(stride[i]));
+        int64_t step = 0;
+        if (__builtin_mul_overflow(stride[i], n[i] - 1, &step) || __builtin_add_overflow(reach, step, &reach) ||
+            reach > (int64_t(1) << 60))
+            return fail(PC_ERR_SHAPE, "%s: strides reach too far", name);
+        kept[i] = stride[i];
+    }
+    if (output && !empty) {  // no two elements at one place: each axis steps over all that lies within it
+        int64_t inner = dim;
+        bool done[3] = {n[0] <= 1, n[1] <= 1, n[2] <= 1};
+        for (int pass = 0; pass < 3; ++pass) {
+            int at = -1;
+            for (int i = 0; i < 3; ++i)
+                if (!done[i] && (at < 0 || stride[i] < stride[at])) at = i;
+            if (at < 0) break;
+            done[at] = true;
+            if (stride[at] < inner)
+                return fail(PC_ERR_SHAPE, "%s: an output's elements overlap (stride %lld)", name,
+                            static_cast<long long>(stride[at]));
+            inner += stride[at] * (n[at] - 1);
+        }
+    }
+    out->b = kept[0];
+    out->t = kept[1];
+    out->h = kept[2];
+    return PC_OK;
+}
+
+// Checks sizes and strides; on success fills what a launch needs but the pointers.
+pc_status check_attention(const pc_attention *a, bool backward, pc::AttnArgs *out) {
+    if (!a) return fail(PC_ERR_NULL, "the attention's sizes are NULL");
+    pc_status st = check_dtype_dim(a->dtype, a->dim);
+    if (st != PC_OK) return st;
+    if (a->n_kv < 0 || a->group < 0 || a->len_q < 0 || a->len_k < 0 || a->len_k > (1 << 30))
+        return fail(PC_ERR_SHAPE, "sizes out of range (n_kv %d, group %d, len_q %d, len_k %d)", a->n_kv, a->group,
+                    a->len_q, a->len_k);
+    if (a->heads < 1 || a->heads_kv < 1 || a->heads % a->heads_kv != 0)
+        return fail(PC_ERR_SHAPE, "%d key heads must divide %d query heads", a->heads_kv, a->heads);
+    if (!(a->scale > 0.f) || !isfinite(a->scale))
+        return fail(PC_ERR_PARAM, "scale = %g must be finite and > 0", static_cast<double>(a->scale));
+    const int64_t batch = static_cast<int64_t>(a->n_kv) * a->group;
+    const int64_t rep = a->heads / a->heads_kv;
+    int64_t rows = static_cast<int64_t>(a->group) * a->len_q;  // below 2^62
+    if (__builtin_mul_overflow(rows, rep, &rows) || rows > 0x7FFFFFFFLL - 256)
+        return fail(PC_ERR_SHAPE, "2^31 or more query rows share a key head");
+    const int64_t tiles_q = (rows + 31) / 32, tiles_k = (static_cast<int64_t>(a->len_k) + 31) / 32;
+    int64_t blocks = static_cast<int64_t>(a->n_kv) * a->heads_kv;
+    if (__builtin_mul_overflow(blocks, (tiles_q > tiles_k ? tiles_q : tiles_k) + 1024, &blocks) || blocks > 0x7FFFFFFFLL)
+        return fail(PC_ERR_SHAPE, "2^31 or more workgroups");
+    pc::AttnArgs r;
+    memset(&r, 0, sizeof r);
+    struct {
+        const char *name;
+        const pc_strides *s;
+        pc::HeadStrides *to;
+        bool query, output, needed;
+    } t[] = {{"q", &a->q, &r.sq, true, false, true},       {"k", &a->k, &r.sk, false, false, true},
+             {"v", &a->v, &r.sv, false, false, true},      {"out", &a->out, &r.so, true, !backward, true},
+             {"dout", &a->dout, &r.sdo, true, false, backward}, {"dq", &a->dq, &r.sdq, true, true, backward},
+             {"dk", &a->dk, &r.sdk, false, true, backward},     {"dv", &a->dv, &r.sdv, false, true, backward}};
+    for (const auto &x : t) {
+        if (!x.needed) continue;
+        st = check_strides(x.name, *x.s, a->dtype, x.query ? batch : a->n_kv, x.query ? a->len_q : a->len_k,
+                           x.query ? a->heads : a->heads_kv, a->dim, x.output, x.to);
+        if (st != PC_OK) return st;
+    }
+    r.n_kv = a->n_kv;
+    r.group = a->group;
+    r.Lq = a->len_q;
+    r.Lk = a->len_k;
+    r.H = a->heads;
+    r.Hk = a->heads_kv;
+    r.D = a->dim;
+    r.rows = static_cast<uint32_t>(rows);
+    r.rep = pc::fast_div(static_cast<uint32_t>(rep));
+    r.len_q = pc::fast_div(a->len_q > 0 ? static_cast<uint32_t>(a->len_q) : 1u);
+    r.heads_kv = pc::fast_div(static_cast<uint32_t>(a->heads_kv));
+    r.scale = a->scale;
+    r.scale_log2 = a->scale * pc::kLog2e;
+    *out = r;
+    return PC_OK;
+}
+
+pc_status check_workspace(const void *workspace, int64_t given, int64_t need) {
+    if (need == 0) return PC_OK;
+    if (!workspace) return fail(PC_ERR_NULL, "a workspace of %lld bytes is required", static_cast<long long>(need));
+    if (given < need)
+        return fail(PC_ERR_SHAPE, "workspace of %lld bytes, %lld are required", static_cast<long long>(given),
+                    static_cast<long long>(need));
+    if (!aligned16(workspace)) return fail(PC_ERR_ALIGN, "workspace not 16-byte aligned");
+    return PC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pc_status pc_cross_attention_workspace(const pc_attention *a, int32_t backward, int64_t *bytes) {
+    if (!bytes) return fail(PC_ERR_NULL, "bytes is NULL");
+    pc::AttnArgs r;
+    const pc_status st = check_attention(a, backward != 0, &r);
+    if (st != PC_OK) return st;
+    *bytes = backward ? pc::attn_bwd_workspace(r, a->dtype) : pc::attn_fwd_workspace(r, a->dtype);
+    return ok();
+}
+
+pc_status pc_cross_attention(const pc_attention *a, const void *q, const void *k, const void *v, const int32_t *kv_len,
+                             const uint8_t *key_mask, void *out, float *lse, void *workspace, int64_t workspace_bytes,
+                             void *stream) {
+    pc::AttnArgs r;
+    pc_status st = check_attention(a, false, &r);
+    if (st != PC_OK) return st;
+    if (r.n_kv == 0 || r.rows == 0) return ok();  // no output element
+    if (!q || !out || (r.Lk > 0 && (!k || !v))) return fail(PC_ERR_NULL, "q, k, v and out are required");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse) || !aligned4(kv_len))
+        return fail(PC_ERR_ALIGN, "device arrays must be 16-byte aligned (kv_len: 4)");
+    st = check_workspace(workspace, workspace_bytes, pc::attn_fwd_workspace(r, a->dtype));
+    if (st != PC_OK) return st;
+    r.q = q;
+    r.k = k;
+    r.v = v;
+    r.o = out;
+    r.lse = lse;
+    r.kv_len = kv_len;
+    r.key_mask = key_mask;
+    return hip_status(pc::launch_attn_fwd(r, a->dtype, static_cast<char *>(workspace), static_cast<hipStream_t>(stream)),
+                      "attention launch");
+}
+
+pc_status pc_cross_attention_backward(const pc_attention *a, const void *q, const void *k, const void *v,
+                                      const void *out, const float *lse, const void *dout, const int32_t *kv_len,
+                                      const uint8_t *key_mask, void *dq, void *dk, void *dv, void *workspace,
+                                      int64_t workspace_bytes, void *stream) {
+    pc::AttnArgs r;
+    pc_status st = check_attention(a, true, &r);
+    if (st != PC_OK) return st;
+    if (r.n_kv == 0 || (r.rows == 0 && r.Lk == 0)) return ok();  // no gradient element
+    if (r.rows > 0 && (!q || !out || !lse || !dout || !dq))
+        return fail(PC_ERR_NULL, "q, out, lse, dout and dq are required");
+    if (r.Lk > 0 && (!k || !v || !dk || !dv)) return fail(PC_ERR_NULL, "k, v, dk and dv are required");
+    const void *all[] = {q, k, v, out, lse, dout, dq, dk, dv};
+    for (const void *p : all)
+        if (!aligned16(p)) return fail(PC_ERR_ALIGN, "device arrays must be 16-byte aligned");
+    if (!aligned4(kv_len)) return fail(PC_ERR_ALIGN, "kv_len must be 4-byte aligned");
+    st = check_workspace(workspace, workspace_bytes, pc::attn_bwd_workspace(r, a->dtype));
+    if (st != PC_OK) return st;
+    r.q = q;
+    r.k = k;
+    r.v = v;
+    r.o_in = out;
+    r.lse = const_cast<float *>(lse);  // read only in the backward kernels
+    r.dout = dout;
+    r.kv_len = kv_len;
+    r.key_mask = key_mask;
+    r.dq = dq;
+    r.dk = dk;
+    r.dv = dv;
+    return hip_status(pc::launch_attn_bwd(r, a->dtype, static_cast<char *>(workspace), static_cast<hipStream_t>(stream)),
+                      "attention gradient launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes and strides of a side; pointers too where `pointers`.
+pc_status check_side(const char *name, const pc_norm_side *s, pc_dtype dtype, int32_t dim, bool backward, bool pointers,
+                     pc::NormSide *out) {
+    memset(out, 0, sizeof *out);
+    out->len = out->heads = pc::fast_div(1);
+    if (!s) return PC_OK;
+    if (s->batch < 0 || s->len < 0 || s->heads < 1)
+        return fail(PC_ERR_SHAPE, "%s: sizes out of range (batch %d, len %d, heads %d)", name, s->batch, s->len,
+                    s->heads);
+    const int64_t tokens = static_cast<int64_t>(s->batch) * s->len;
+    if (tokens > 0x7FFFFFFFLL - 256) return fail(PC_ERR_SHAPE, "%s: 2^31 or more tokens", name);
+    if (s->heads > (1 << 20)) return fail(PC_ERR_SHAPE, "%s: %d heads", name, s->heads);
+    pc_status st = check_strides(name, s->sx, dtype, s->batch, s->len, s->heads, dim, false, &out->sx);
+    if (st == PC_OK && !backward)
+        st = check_strides(name, s->sy, dtype, s->batch, s->len, s->heads, dim, true, &out->sy);
+    if (st == PC_OK && backward)
+        st = check_strides(name, s->sdy, dtype, s->batch, s->len, s->heads, dim, false, &out->sdy);
+    if (st == PC_OK && backward)
+        st = check_strides(name, s->sdx, dtype, s->batch, s->len, s->heads, dim, true, &out->sdx);
+    if (st != PC_OK) return st;
+    if (s->positions && s->positions_stride < 0)
+        return fail(PC_ERR_SHAPE, "%s: negative stride of positions", name);
+    out->tokens = tokens;
+    out->len = pc::fast_div(s->len > 0 ? static_cast<uint32_t>(s->len) : 1u);
+    out->heads = pc::fast_div(static_cast<uint32_t>(s->heads));
+    if (!pointers) return PC_OK;
+    if (tokens > 0 && (!s->x || (backward ? !s->dy || !s->dx : !s->y)))
+        return fail(PC_ERR_NULL, "%s: x and %s are required", name, backward ? "dy, dx" : "y");
+    const void *all[] = {s->x, s->weight, backward ? nullptr : s->y, backward ? s->dy : nullptr,
+                         backward ? s->dx : nullptr, backward ? s->dweight : nullptr};
+    for (const void *p : all)
+        if (!aligned16(p)) return fail(PC_ERR_ALIGN, "%s: device arrays must be 16-byte aligned", name);
+    if (tokens > 0 && (backward ? s->dx == s->dy && !same(out->sdx, out->sdy) : s->y == s->x && !same(out->sy, out->sx)))
+        return fail(PC_ERR_SHAPE, "%s: in place with other strides", name);
+    if (!aligned4(s->positions)) return fail(PC_ERR_ALIGN, "%s: positions must be 4-byte aligned", name);
+    out->x = s->x;
+    out->y = s->y;
+    out->w = s->weight;
+    out->pos = s->positions;
+    out->pos_b = s->positions_stride;
+    out->dy = s->dy;
+    out->dx = s->dx;
+    out->dw = backward ? s->dweight : nullptr;
+    return PC_OK;
+}
+
+pc_status check_norm(const pc_norm_side *q, const pc_norm_side *k, pc_dtype dtype, int32_t dim, int32_t rot_dim,
+                     bool backward, bool pointers, pc::NormArgs *out) {
+    if (!q && !k) return fail(PC_ERR_NULL, "queries and keys are both NULL");
+    pc_status st = check_dtype_dim(dtype, dim);
+    if (st != PC_OK) return st;
+    if (rot_dim < 0 || rot_dim > dim || rot_dim % 16 != 0)
+        return fail(PC_ERR_SHAPE, "rot_dim %d is not a multiple of 16 in 0..%d", rot_dim, dim);
+    out->D = dim;
+    out->half = rot_dim / 2;
+    out->inv_d = 1.f / static_cast<float>(dim);
+    st = check_side("queries", q, dtype, dim, backward, pointers, &out->side[0]);
+    return st != PC_OK ? st : check_side("keys", k, dtype, dim, backward, pointers, &out->side[1]);
+}
+
+// Frequencies in turns per position, 64-bit fixed point, and eps.
+pc_status check_angles(const double *freqs, float eps, pc::NormArgs *a) {
+    if (!(eps >= 0.f) || !isfinite(eps)) return fail(PC_ERR_PARAM, "eps = %g must be finite and >= 0", static_cast<double>(eps));
+    if (a->half > 0 && !freqs) return fail(PC_ERR_NULL, "freqs is NULL");
+    const double turn = 6.283185307179586;
+    for (int i = 0; i < a->half; ++i) {
+        if (!(fabs(freqs[i]) <= turn)) return fail(PC_ERR_PARAM, "freqs[%d] = %g outside [-2 pi, 2 pi]", i, freqs[i]);
+        double f = freqs[i] / turn;  // in [-1, 1]; whole turns change nothing
+        f -= floor(f);               // [0, 1]: 1 where a tiny negative f rounds up
+        a->turns[i] = f < 1.0 ? static_cast<uint64_t>(ldexp(f, 64)) : 0u;
+    }
+    a->eps = eps;
+    return PC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pc_status pc_qk_norm_rope(const pc_norm_side *q, const pc_norm_side *k, pc_dtype dtype, int32_t dim, int32_t rot_dim,
+                          const double *freqs, int32_t interleaved, float eps, void *stream) {
+    pc::NormArgs a;
+    memset(&a, 0, sizeof a);
+    pc_status st = check_norm(q, k, dtype, dim, rot_dim, false, true, &a);
+    if (st == PC_OK) st = check_angles(freqs, eps, &a);
+    if (st != PC_OK) return st;
+    return hip_status(pc::launch_norm_fwd(a, dtype, interleaved != 0, static_cast<hipStream_t>(stream)), "norm launch");
+}
+
+pc_status pc_qk_norm_rope_workspace(const pc_norm_side *q, const pc_norm_side *k, pc_dtype dtype, int32_t dim,
+                                    int32_t rot_dim, int64_t *bytes) {
+    if (!bytes) return fail(PC_ERR_NULL, "bytes is NULL");
+    pc::NormArgs a;
+    memset(&a, 0, sizeof a);
+    const pc_status st = check_norm(q, k, dtype, dim, rot_dim, true, false, &a);
+    if (st != PC_OK) return st;
+    *bytes = pc::norm_bwd_workspace(a, dtype);
+    return ok();
+}
+
+pc_status pc_qk_norm_rope_backward(const pc_norm_side *q, const pc_norm_side *k, pc_dtype dtype, int32_t dim,
+                                   int32_t rot_dim, const double *freqs, int32_t interleaved, float eps,
+                                   void *workspace, int64_t workspace_bytes, void *stream) {
+    pc::NormArgs a;
+    memset(&a, 0, sizeof a);
+    pc_status st = check_norm(q, k, dtype, dim, rot_dim, true, true, &a);
+    if (st == PC_OK) st = check_angles(freqs, eps, &a);
+    if (st == PC_OK) st = check_workspace(workspace, workspace_bytes, pc::norm_bwd_workspace(a, dtype));
+    if (st != PC_OK) return st;
+    return hip_status(pc::launch_norm_bwd(a, dtype, interleaved != 0, static_cast<char *>(workspace),
+                                          static_cast<hipStream_t>(stream)),
+                      "norm gradient launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,357 @@
+// Shared pieces of the cross-attention kernels: arguments, the row index of
+// queries that share one key head, tiles staged in LDS, and the 32x32 matrix
+// core operands.
+//
+// Rows.  The queries that read key head j of encoder state r are all maps of
+// the state's group, all their tokens and the H / Hk query heads of j; they
+// form one matrix of M = group len_q H / Hk rows, row = (s len_q + i) rep + hr.
+// So one map of 64 tokens, 512 maps that share a region and a single token of
+// 8 heads are the same product with another M, and K and V are staged once for
+// all of them.
+//
+// Matrix operands.  A fragment is 16 bytes per lane: lane l holds row (or
+// column) l & 31 and, of a block of 2 EPC contraction values, the EPC of half
+// l >> 5 (EPC = 8 values of 16 bits, one 32x32x16 instruction; 4 floats, four
+// 32x32x2 instructions).  The accumulator of a 32x32 product holds in register
+// r of lane l: row 8 (r / 4) + 4 (l >> 5) + r % 4, column l & 31.  A product's
+// accumulator, rounded, is therefore the second operand of the next product as
+// it stands (contraction over its rows, in this order): probabilities never
+// pass through LDS.  The first operand of that product is read from the same
+// row-major tile, transposed on the way (ds_read_b64_tr_b16 for 16-bit types).
+#pragma once
+
+#include <type_traits>
+
+#include "common.hpp"
+
+namespace pc {
+
+struct HeadStrides {
+    int64_t b, t, h;  // elements between batches, tokens, heads
+};
+
+// n / d for n < 2^31 by a multiplication (Granlund and Montgomery, PLDI '94);
+// d = 0 (an axis without entries, nothing is launched over it) counts as 1.
+struct FastDiv {
+    uint32_t mul, shift, d;
+};
+inline FastDiv fast_div(uint32_t d) {
+    if (d == 0) d = 1;
+    FastDiv f{0, 0, d};
+    while ((uint64_t(1) << f.shift) < d) ++f.shift;
+    f.mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << f.shift) - d)) / d + 1);
+    return f;
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv &f) {
+    return (__umulhi(n, f.mul) + n) >> f.shift;
+}
+
+struct AttnArgs {
+    const void *q, *k, *v, *dout;
+    const void *o_in;
+    void *o, *dq, *dk, *dv;
+    float *lse;
+    const int32_t *kv_len;
+    const uint8_t *key_mask;
+    float *part;        // workspace: partial sums of a split (see the kernels)
+    float *part_ml;     // forward split: running maximum and sum
+    float *delta;       // backward: rowsum(dout o out) per row
+    HeadStrides sq, sk, sv, so, sdo, sdq, sdk, sdv;
+    FastDiv rep, len_q, heads_kv, n_split, n_tiles;
+    int32_t n_kv, group, Lq, Lk, H, Hk, D;
+    uint32_t rows;          // M
+    uint32_t split_tiles;   // staged tiles per split
+    float scale;            // softmax scale
+    float scale_log2;       // scale log2(e)
+};
+
+// Element types, as the ABI numbers them (pc.h).
+constexpr int32_t kF32 = 0, kBf16 = 1, kF16 = 2;
+struct Bf16 {
+    static constexpr int kSize = 2;
+};
+struct F16 {
+    static constexpr int kSize = 2;
+};
+struct F32 {
+    static constexpr int kSize = 4;
+};
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32v4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+template <class T>
+__device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c);
+template <>
+__device__ __forceinline__ f32x16 mma<Bf16>(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16 mma<F16>(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+template <>
+__device__ __forceinline__ f32x16 mma<F32>(u32x4 a, u32x4 b, f32x16 c) {
+    const f32v4 x = __builtin_bit_cast(f32v4, a), y = __builtin_bit_cast(f32v4, b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[j], y[j], c, 0, 0, 0);
+    return c;
+}
+
+// Rounds to nearest even, two values to a dword.
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<Bf16>(float a, float b) {
+    typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+    const v2 p = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    return __builtin_bit_cast(uint32_t, p);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<F16>(float a, float b) {
+    typedef _Float16 v2 __attribute__((ext_vector_type(2)));
+    const v2 p = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
+    return __builtin_bit_cast(uint32_t, p);
+}
+template <class T>
+__device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b);
+template <>
+__device__ __forceinline__ void unpack2<Bf16>(uint32_t w, float &a, float &b) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xFFFF0000u);
+}
+template <>
+__device__ __forceinline__ void unpack2<F16>(uint32_t w, float &a, float &b) {
+    typedef _Float16 v2 __attribute__((ext_vector_type(2)));
+    const v2 p = __builtin_bit_cast(v2, w);
+    a = static_cast<float>(p[0]);
+    b = static_cast<float>(p[1]);
+}
+
+// The 16 bytes of a fragment or chunk as floats.
+template <class T>
+__device__ __forceinline__ void unpack_chunk(u32x4 w, float (&x)[16 / T::kSize]) {
+    if constexpr (T::kSize == 4) {
+        const f32v4 f = __builtin_bit_cast(f32v4, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = f[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) unpack2<T>(w[j], x[2 * j], x[2 * j + 1]);
+    }
+}
+
+// Contraction block t of an accumulator as the second operand of a product.
+template <class T>
+__device__ __forceinline__ u32x4 pack_frag(const f32x16 &p, int t) {
+    u32x4 w;
+    if constexpr (T::kSize == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(p[4 * t + j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack2<T>(p[8 * t + 2 * j], p[8 * t + 2 * j + 1]);
+    }
+    return w;
+}
+
+// Four consecutive values, rounded, to a 4-element-aligned address.
+template <class T>
+__device__ __forceinline__ void store4(void *base, int64_t element, float a, float b, float c, float d) {
+    if constexpr (T::kSize == 4) {
+        *reinterpret_cast<f32v4 *>(static_cast<float *>(base) + element) = f32v4{a, b, c, d};
+    } else {
+        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(base) + element) = u32x2{pack2<T>(a, b), pack2<T>(c, d)};
+    }
+}
+
+// The value of lane l ^ 32.
+__device__ __forceinline__ float other_half(float x) {
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    // r.x: lanes 0-31 of x in both halves; r.y: lanes 32-63 in both halves
+    return __uint_as_float((threadIdx.x & 32) ? r.x : r.y);
+}
+
+// exp2 and log2 of the hardware (1 ulp; results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr int kAttnThreads = 256;
+constexpr int kAttnWaves = kAttnThreads / 64;
+
+// A tile of BN rows of up to DP values, row-major in LDS.  Its 16-byte chunks
+// are permuted within each row by an XOR of the chunk index with bits of the
+// row, so that neither the row reads (32 rows, one chunk) nor the transposed
+// reads (4 rows, 4 chunks) of a wavefront fall on the same banks.
+template <class T, int DP>
+struct Tile {
+    static constexpr int kSize = T::kSize;
+    static constexpr int EPC = 16 / kSize;      // elements per chunk
+    static constexpr int CH = DP / EPC;         // chunks per row
+    static constexpr int FR = CH / 2;           // fragments over a row
+    static constexpr int ROWB = DP * kSize;     // bytes per row
+    static constexpr int BN = kSize == 4 ? 32 : 64;  // rows per tile
+    static constexpr int SUB = BN / 32;
+    static constexpr int NB = 32 / (2 * EPC);   // contraction blocks of 32 rows
+    static constexpr int DT = DP / 32;          // 32-wide column tiles
+    static constexpr int NCH = BN * CH / kAttnThreads;  // chunks per lane when a workgroup stages a tile
+    static constexpr int kBytes = BN * ROWB;
+
+    __device__ static __forceinline__ int swz(int row, int c) {
+        constexpr int s = (CH == 4 || CH == 12) ? 1 : 0;  // rows of 64 and 192 bytes: bank parity from row bit 0
+        const int r = row >> s;
+        if constexpr (CH % 8 == 0)
+            return c ^ ((r & 1) | ((r & 4) >> 1) | ((r & 2) << 1));
+        else
+            return c ^ (r & 3);
+    }
+    __device__ static __forceinline__ int at(int row, int c) { return row * ROWB + swz(row, c) * 16; }
+
+    // Fragment f of row `row`.
+    __device__ static __forceinline__ u32x4 frag(const char *tile, int row, int f, int half) {
+        return *reinterpret_cast<const u32x4 *>(tile + at(row, 2 * f + half));
+    }
+    // First operand with the tile's columns d0 .. d0 + 31 as its rows and the
+    // contraction over 2 EPC tile rows from row0 on, in accumulator order.
+    __device__ static __forceinline__ u32x4 frag_t(const char *tile, int row0, int d0, int lane) {
+        if constexpr (kSize == 4) {
+            const int d = d0 + (lane & 31), row = row0 + 4 * (lane >> 5);
+            u32x4 w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = *reinterpret_cast<const uint32_t *>(tile + at(row + j, d >> 2) + (d & 3) * 4);
+            return w;
+        } else {
+            const int i = lane & 15, row = row0 + 4 * (lane >> 5) + (i >> 2);
+            const int d = d0 + 16 * ((lane >> 4) & 1) + (i & 3) * 4;
+            typedef __attribute__((address_space(3))) i16x4 *lds_ptr;
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_ptr)(tile + at(row, d >> 3) + (d & 4) * 2));
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_ptr)(tile + at(row + 8, d >> 3) + (d & 4) * 2));
+            const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+            return u32x4{a.x, a.y, b.x, b.y};
+        }
+    }
+};
+
+// Chunk c of a row of `dim` values at `row` (elements); zero past dim.
+template <class T>
+__device__ __forceinline__ u32x4 load_chunk(const void *base, int64_t row, int c, int dim, bool valid) {
+    constexpr int EPC = 16 / T::kSize;
+    u32x4 w = {0u, 0u, 0u, 0u};
+    if (valid && c * EPC < dim)
+        w = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(base) + (row + c * EPC) * T::kSize);
+    return w;
+}
+
+// The chunks of one tile that this lane stages, held in registers between the
+// global loads and the LDS stores.
+template <class T, int DP>
+struct Staged {
+    using TL = Tile<T, DP>;
+    u32x4 w[TL::NCH];
+    __device__ __forceinline__ void store(char *tile) const {
+#pragma unroll
+        for (int i = 0; i < TL::NCH; ++i) {
+            const int id = static_cast<int>(threadIdx.x) + i * kAttnThreads;
+            *reinterpret_cast<u32x4 *>(tile + TL::at(id / TL::CH, id % TL::CH)) = w[i];
+        }
+    }
+    // Rows row0 .. row0 + BN - 1 of keys or values; those whose bit of `valid`
+    // is clear read as zero, so nothing an unattended place holds (NaN, too)
+    // reaches a product.
+    __device__ __forceinline__ void load_keys(const void *base, int64_t off, int64_t stride, int row0, uint64_t valid,
+                                              int dim) {
+#pragma unroll
+        for (int i = 0; i < TL::NCH; ++i) {
+            const int id = static_cast<int>(threadIdx.x) + i * kAttnThreads;
+            const int r = id / TL::CH;
+            w[i] = load_chunk<T>(base, off + (row0 + r) * stride, id % TL::CH, dim, (valid >> r) & 1);
+        }
+    }
+};
+
+// Element offset of query row `row` of (state r, key head j), without the
+// batch and head offsets of (r, j) itself.
+__device__ __forceinline__ int64_t row_offset(uint32_t row, const AttnArgs &a, const HeadStrides &s) {
+    const uint32_t t = div_by(row, a.rep), hr = row - t * a.rep.d;
+    const uint32_t m = div_by(t, a.len_q), i = t - m * a.len_q.d;
+    return static_cast<int64_t>(m) * s.b + static_cast<int64_t>(i) * s.t + static_cast<int64_t>(hr) * s.h;
+}
+__device__ __forceinline__ int64_t pair_offset(uint32_t r, uint32_t j, const AttnArgs &a, const HeadStrides &s) {
+    return static_cast<int64_t>(r) * a.group * s.b + static_cast<int64_t>(j) * a.rep.d * s.h;
+}
+// Index of the row in lse [batch][len_q][heads].
+__device__ __forceinline__ int64_t lse_index(uint32_t r, uint32_t j, uint32_t row, const AttnArgs &a) {
+    const uint32_t t = div_by(row, a.rep), hr = row - t * a.rep.d;
+    return (static_cast<int64_t>(r) * a.group * a.Lq + t) * a.H + j * a.rep.d + hr;
+}
+
+// Keys of state r that may be attended: a prefix of Lk.
+__device__ __forceinline__ int keys_of(uint32_t r, const AttnArgs &a) {
+    if (!a.kv_len) return a.Lk;
+    const int n = a.kv_len[r];
+    return n < 0 ? 0 : (n > a.Lk ? a.Lk : n);
+}
+// Bit i: key key0 + i is attended (i < BN).
+template <int BN>
+__device__ __forceinline__ uint64_t valid_keys(uint32_t r, int key0, int end, const AttnArgs &a) {
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    bool ok = lane < BN && key0 + lane < end;
+    if (a.key_mask && ok) ok = a.key_mask[static_cast<int64_t>(r) * a.Lk + key0 + lane] != 0;
+    return __ballot(ok);
+}
+
+// Calls f(type, integral_constant<padded dim>) for the kernel instance that
+// holds heads of `dim` values.
+template <class F>
+void for_dtype_dim(int32_t dtype, int32_t dim, F &&f) {
+    const auto dims = [&](auto type) {
+        if (dim <= 32) f(type, std::integral_constant<int, 32>{});
+        else if (dim <= 64) f(type, std::integral_constant<int, 64>{});
+        else if (dim <= 96) f(type, std::integral_constant<int, 96>{});
+        else f(type, std::integral_constant<int, 128>{});
+    };
+    if (dtype == kBf16) dims(Bf16{});
+    else if (dtype == kF16) dims(F16{});
+    else dims(F32{});
+}
+
+// How a grid of (pairs) x (tiles of the parallel axis) is split over the long
+// axis of `steps` staged tiles when it alone would not fill the card: to about
+// two workgroups per compute unit, no split below `least` steps.
+struct AttnPlan {
+    int64_t n_tiles, n_split, split_tiles;
+};
+inline AttnPlan attn_plan(int64_t pairs, int64_t n_tiles, int64_t steps, int64_t least) {
+    constexpr int64_t kWant = 512;
+    AttnPlan p{n_tiles, 1, steps > 0 ? steps : 1};
+    const int64_t blocks = pairs * n_tiles;
+    if (blocks <= 0 || blocks >= kWant || steps <= least) return p;
+    int64_t n = (kWant + blocks - 1) / blocks;
+    const int64_t most = steps / least;
+    if (n > most) n = most;
+    if (n < 2) return p;
+    p.split_tiles = (steps + n - 1) / n;
+    p.n_split = (steps + p.split_tiles - 1) / p.split_tiles;
+    return p;
+}
+inline int64_t round16(int64_t bytes) { return (bytes + 15) & ~static_cast<int64_t>(15); }
+
+// Launchers (api_attn.hip calls them after validation).
+int64_t attn_fwd_workspace(const AttnArgs &a, int32_t dtype);
+hipError_t launch_attn_fwd(AttnArgs a, int32_t dtype, char *workspace, hipStream_t stream);
+int64_t attn_bwd_workspace(const AttnArgs &a, int32_t dtype);
+hipError_t launch_attn_bwd(AttnArgs a, int32_t dtype, char *workspace, hipStream_t stream);
+
+}  // namespace pc

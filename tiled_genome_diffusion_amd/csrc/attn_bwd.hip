@@ -1,0 +1,370 @@
+// Cross attention, backward: dQ, dK and dV from the forward's inputs, output
+// and log-sum-exp, over the rows of attn.hpp.
+//   P = exp(S - lse), dP = dO V^T, delta = rowsum(dO o O), dS = P o (dP - delta),
+//   dQ = scale dS K, dK = scale dS^T Q, dV = P^T dO.
+// P and dS are rounded to the input type as operands of their products; sums,
+// P, delta and lse are float32.  Every sum has a fixed order: no atomics.
+#include "attn.hpp"
+#include "launch.hpp"
+
+namespace pc {
+namespace {
+
+// dQ (and delta, for the kernel below): 4 wavefronts of 32 rows, keys and
+// values in LDS tiles, as the forward.
+template <class T, int DP, bool SPLIT>
+__global__ __launch_bounds__(kAttnThreads) void k_attn_dq(const AttnArgs a, int64_t block0) {
+    using TL = Tile<T, DP>;
+    __shared__ __align__(16) char s_k[2][TL::kBytes];
+    __shared__ __align__(16) char s_v[2][TL::kBytes];
+    const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
+    const int half = lane >> 5, col = lane & 31;
+    const uint32_t bid = static_cast<uint32_t>(block0) + xcd_remap(blockIdx.x, gridDim.x);
+    const uint32_t ps = div_by(bid, a.n_tiles), rt = bid - ps * a.n_tiles.d;
+    const uint32_t pair = div_by(ps, a.n_split), split = ps - pair * a.n_split.d;
+    const uint32_t r = div_by(pair, a.heads_kv), j = pair - r * a.heads_kv.d;
+
+    const uint32_t row = rt * (kAttnWaves * 32) + wave * 32 + col;
+    const bool row_ok = row < a.rows;
+    u32x4 qf[TL::FR], gf[TL::FR];
+    float delta = 0.f, lse2 = INFINITY;  // rows past the end: P = 0
+    {
+        const int64_t offq = pair_offset(r, j, a, a.sq) + (row_ok ? row_offset(row, a, a.sq) : 0);
+        const int64_t offg = pair_offset(r, j, a, a.sdo) + (row_ok ? row_offset(row, a, a.sdo) : 0);
+        const int64_t offo = pair_offset(r, j, a, a.so) + (row_ok ? row_offset(row, a, a.so) : 0);
+#pragma unroll
+        for (int f = 0; f < TL::FR; ++f) {
+            qf[f] = load_chunk<T>(a.q, offq, 2 * f + half, a.D, row_ok);
+            gf[f] = load_chunk<T>(a.dout, offg, 2 * f + half, a.D, row_ok);
+            float g[TL::EPC], o[TL::EPC];
+            unpack_chunk<T>(gf[f], g);
+            unpack_chunk<T>(load_chunk<T>(a.o_in, offo, 2 * f + half, a.D, row_ok), o);
+#pragma unroll
+            for (int i = 0; i < TL::EPC; ++i) delta = fmaf(g[i], o[i], delta);
+        }
+        delta += other_half(delta);
+        if (row_ok) lse2 = a.lse[lse_index(r, j, row, a)] * kLog2e;
+        if (row_ok && half == 0 && split == 0) a.delta[static_cast<int64_t>(pair) * a.rows + row] = delta;
+    }
+    f32x16 dq[TL::DT];
+#pragma unroll
+    for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dq[d][i] = 0.f;
+
+    const int n_keys = keys_of(r, a);
+    const int first = static_cast<int>(split * a.split_tiles) * TL::BN;
+    const int64_t span = static_cast<int64_t>(a.split_tiles) * TL::BN;
+    const int end = static_cast<int>(first + span < n_keys ? first + span : n_keys);
+    const int64_t koff = static_cast<int64_t>(r) * a.sk.b + static_cast<int64_t>(j) * a.sk.h;
+    const int64_t voff = static_cast<int64_t>(r) * a.sv.b + static_cast<int64_t>(j) * a.sv.h;
+
+    Staged<T, DP> gk, gv;
+    uint64_t valid = 0;
+    if (first < end) {
+        valid = valid_keys<TL::BN>(r, first, end, a);
+        gk.load_keys(a.k, koff, a.sk.t, first, valid, a.D);
+        gv.load_keys(a.v, voff, a.sv.t, first, valid, a.D);
+        gk.store(s_k[0]);
+        gv.store(s_v[0]);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int key0 = first; key0 < end; key0 += TL::BN, buf ^= 1) {
+        uint64_t next = 0;
+        const bool more = key0 + TL::BN < end;
+        if (more) {
+            next = valid_keys<TL::BN>(r, key0 + TL::BN, end, a);
+            gk.load_keys(a.k, koff, a.sk.t, key0 + TL::BN, next, a.D);
+            gv.load_keys(a.v, voff, a.sv.t, key0 + TL::BN, next, a.D);
+        }
+#pragma unroll
+        for (int t = 0; t < TL::SUB; ++t) {
+            const uint32_t live = static_cast<uint32_t>(valid >> (32 * t));
+            if (live == 0) continue;
+            f32x16 s, g;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = g[i] = 0.f;
+#pragma unroll
+            for (int f = 0; f < TL::FR; ++f) {
+                s = mma<T>(TL::frag(s_k[buf], t * 32 + col, f, half), qf[f], s);
+                g = mma<T>(TL::frag(s_v[buf], t * 32 + col, f, half), gf[f], g);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = exp2_hw(fmaf(s[i], a.scale_log2, -lse2)) * (g[i] - delta);
+            if (live != 0xFFFFFFFFu) {
+                const uint32_t bits = live >> (4 * half);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!((bits >> (8 * (i / 4) + i % 4)) & 1)) s[i] = 0.f;
+            }
+#pragma unroll
+            for (int b = 0; b < TL::NB; ++b) {
+                const u32x4 p = pack_frag<T>(s, b);
+#pragma unroll
+                for (int d = 0; d < TL::DT; ++d)
+                    dq[d] = mma<T>(TL::frag_t(s_k[buf], t * 32 + b * 2 * TL::EPC, d * 32, lane), p, dq[d]);
+            }
+        }
+        if (more) {
+            gk.store(s_k[buf ^ 1]);
+            gv.store(s_v[buf ^ 1]);
+        }
+        valid = next;
+        __syncthreads();
+    }
+    if (!row_ok) return;
+    const int64_t slot = (static_cast<int64_t>(split) * a.n_kv * a.Hk + pair) * a.rows + row;
+    const int64_t off = pair_offset(r, j, a, a.sdq) + row_offset(row, a, a.sdq);
+#pragma unroll
+    for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const int at = d * 32 + 2 * i + 4 * half;
+            if (at >= a.D) continue;
+            const f32v4 x = {dq[d][i] * a.scale, dq[d][i + 1] * a.scale, dq[d][i + 2] * a.scale, dq[d][i + 3] * a.scale};
+            if constexpr (SPLIT)
+                *reinterpret_cast<f32v4 *>(a.part + slot * a.D + at) = x;
+            else
+                store4<T>(a.dq, off + at, x[0], x[1], x[2], x[3]);
+        }
+}
+
+// dK and dV: one workgroup owns 128 keys of one key head (a wavefront 32 of
+// them, K and V in registers) and runs over the rows of its split, queries and
+// output gradients in LDS tiles.  S and dP are formed as rows x keys, so a key
+// is a lane and P and dS are the second operands of dV^T = dO^T P and
+// dK^T = Q^T dS as they stand.
+template <class T, int DP, bool SPLIT>
+__global__ __launch_bounds__(kAttnThreads) void k_attn_dkv(const AttnArgs a, int64_t block0) {
+    using TL = Tile<T, DP>;
+    __shared__ __align__(16) char s_q[2][TL::kBytes];
+    __shared__ __align__(16) char s_g[2][TL::kBytes];
+    __shared__ __align__(16) float s_lse[2][TL::BN], s_delta[2][TL::BN];
+    const int tid = static_cast<int>(threadIdx.x);
+    const int lane = tid & 63, wave = tid >> 6;
+    const int half = lane >> 5, col = lane & 31;
+    const uint32_t bid = static_cast<uint32_t>(block0) + xcd_remap(blockIdx.x, gridDim.x);
+    const uint32_t ps = div_by(bid, a.n_tiles), kt = bid - ps * a.n_tiles.d;
+    const uint32_t pair = div_by(ps, a.n_split), split = ps - pair * a.n_split.d;
+    const uint32_t r = div_by(pair, a.heads_kv), j = pair - r * a.heads_kv.d;
+
+    const int n_keys = keys_of(r, a);
+    const int key = static_cast<int>(kt) * (kAttnWaves * 32) + wave * 32 + col;
+    bool key_ok = key < n_keys;
+    if (a.key_mask && key_ok) key_ok = a.key_mask[static_cast<int64_t>(r) * a.Lk + key] != 0;
+    u32x4 kf[TL::FR], vf[TL::FR];
+    {
+        const int64_t offk = static_cast<int64_t>(r) * a.sk.b + static_cast<int64_t>(j) * a.sk.h + (key_ok ? key * a.sk.t : 0);
+        const int64_t offv = static_cast<int64_t>(r) * a.sv.b + static_cast<int64_t>(j) * a.sv.h + (key_ok ? key * a.sv.t : 0);
+#pragma unroll
+        for (int f = 0; f < TL::FR; ++f) {
+            kf[f] = load_chunk<T>(a.k, offk, 2 * f + half, a.D, key_ok);
+            vf[f] = load_chunk<T>(a.v, offv, 2 * f + half, a.D, key_ok);
+        }
+    }
+    f32x16 dk[TL::DT], dv[TL::DT];
+#pragma unroll
+    for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.f;
+
+    const int64_t first = static_cast<int64_t>(split) * a.split_tiles * TL::BN;
+    const int64_t last = first + static_cast<int64_t>(a.split_tiles) * TL::BN;
+    const int64_t end = static_cast<int>(kt) * (kAttnWaves * 32) >= n_keys ? 0 : (last < a.rows ? last : a.rows);
+    const int64_t baseq = pair_offset(r, j, a, a.sq), baseg = pair_offset(r, j, a, a.sdo);
+    const float *delta = a.delta + static_cast<int64_t>(pair) * a.rows;
+
+    Staged<T, DP> gq, gg;
+    float g_lse = 0.f, g_delta = 0.f;
+    const auto load = [&](int64_t row0) {
+#pragma unroll
+        for (int i = 0; i < TL::NCH; ++i) {
+            const int id = tid + i * kAttnThreads;
+            const int64_t row = row0 + id / TL::CH;
+            const bool ok = row < end;
+            const uint32_t n = ok ? static_cast<uint32_t>(row) : 0u;
+            gq.w[i] = load_chunk<T>(a.q, baseq + row_offset(n, a, a.sq), id % TL::CH, a.D, ok);
+            gg.w[i] = load_chunk<T>(a.dout, baseg + row_offset(n, a, a.sdo), id % TL::CH, a.D, ok);
+        }
+        if (tid < TL::BN) {
+            const bool ok = row0 + tid < end;
+            g_lse = ok ? a.lse[lse_index(r, j, static_cast<uint32_t>(row0 + tid), a)] * kLog2e : INFINITY;
+            g_delta = ok ? delta[row0 + tid] : 0.f;
+        }
+    };
+    const auto put = [&](int b) {
+        gq.store(s_q[b]);
+        gg.store(s_g[b]);
+        if (tid < TL::BN) {
+            s_lse[b][tid] = g_lse;
+            s_delta[b][tid] = g_delta;
+        }
+    };
+    if (first < end) {
+        load(first);
+        put(0);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int64_t row0 = first; row0 < end; row0 += TL::BN, buf ^= 1) {
+        const bool more = row0 + TL::BN < end;
+        if (more) load(row0 + TL::BN);
+#pragma unroll
+        for (int t = 0; t < TL::SUB; ++t) {
+            f32x16 s, g;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = g[i] = 0.f;
+#pragma unroll
+            for (int f = 0; f < TL::FR; ++f) {
+                s = mma<T>(TL::frag(s_q[buf], t * 32 + col, f, half), kf[f], s);
+                g = mma<T>(TL::frag(s_g[buf], t * 32 + col, f, half), vf[f], g);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const f32v4 ls = *reinterpret_cast<const f32v4 *>(&s_lse[buf][t * 32 + 2 * i + 4 * half]);
+                const f32v4 de = *reinterpret_cast<const f32v4 *>(&s_delta[buf][t * 32 + 2 * i + 4 * half]);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float p = key_ok ? exp2_hw(fmaf(s[i + n], a.scale_log2, -ls[n])) : 0.f;
+                    s[i + n] = p;
+                    g[i + n] = key_ok ? p * (g[i + n] - de[n]) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < TL::NB; ++b) {
+                const u32x4 p = pack_frag<T>(s, b), ds = pack_frag<T>(g, b);
+#pragma unroll
+                for (int d = 0; d < TL::DT; ++d) {
+                    dv[d] = mma<T>(TL::frag_t(s_g[buf], t * 32 + b * 2 * TL::EPC, d * 32, lane), p, dv[d]);
+                    dk[d] = mma<T>(TL::frag_t(s_q[buf], t * 32 + b * 2 * TL::EPC, d * 32, lane), ds, dk[d]);
+                }
+            }
+        }
+        if (more) put(buf ^ 1);
+        __syncthreads();
+    }
+    if (key >= a.Lk) return;
+    const int64_t pairs = static_cast<int64_t>(a.n_kv) * a.Hk;
+    const int64_t slot = (static_cast<int64_t>(split) * pairs + pair) * a.Lk + key;
+    float *part_v = a.part + static_cast<int64_t>(a.n_split.d) * pairs * a.Lk * a.D;
+    const int64_t offk = static_cast<int64_t>(r) * a.sdk.b + static_cast<int64_t>(j) * a.sdk.h + key * a.sdk.t;
+    const int64_t offv = static_cast<int64_t>(r) * a.sdv.b + static_cast<int64_t>(j) * a.sdv.h + key * a.sdv.t;
+#pragma unroll
+    for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const int at = d * 32 + 2 * i + 4 * half;
+            if (at >= a.D) continue;
+            const f32v4 x = {dk[d][i] * a.scale, dk[d][i + 1] * a.scale, dk[d][i + 2] * a.scale, dk[d][i + 3] * a.scale};
+            if constexpr (SPLIT) {
+                *reinterpret_cast<f32v4 *>(a.part + slot * a.D + at) = x;
+                *reinterpret_cast<f32v4 *>(part_v + slot * a.D + at) = f32v4{dv[d][i], dv[d][i + 1], dv[d][i + 2], dv[d][i + 3]};
+            } else {
+                store4<T>(a.dk, offk + at, x[0], x[1], x[2], x[3]);
+                store4<T>(a.dv, offv + at, dv[d][i], dv[d][i + 1], dv[d][i + 2], dv[d][i + 3]);
+            }
+        }
+}
+
+// Adds the splits' partial sums [split][pair][n][D] in split order and rounds
+// once.  ROWS: the query rows of dq; otherwise the keys of dk or dv.
+template <bool ROWS>
+__global__ __launch_bounds__(256) void k_attn_sum(const AttnArgs a, const float *part, void *out, HeadStrides so,
+                                                  int32_t dtype, int64_t total, int64_t block0) {
+    const int64_t id = (block0 + blockIdx.x) * 256 + threadIdx.x;
+    if (id >= total) return;
+    const uint32_t n = ROWS ? a.rows : static_cast<uint32_t>(a.Lk), quads = a.D / 4;
+    const int64_t slot = id / quads;
+    const int d = static_cast<int>(id - slot * quads) * 4;
+    const uint32_t pair = static_cast<uint32_t>(slot / n), at = static_cast<uint32_t>(slot - static_cast<int64_t>(pair) * n);
+    const uint32_t r = pair / a.Hk, j = pair - r * a.Hk;
+    f32v4 x = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t s = 0; s < a.n_split.d; ++s)
+        x += *reinterpret_cast<const f32v4 *>(part + (static_cast<int64_t>(s) * a.n_kv * a.Hk * n + slot) * a.D + d);
+    const int64_t off = d + (ROWS ? pair_offset(r, j, a, so) + row_offset(at, a, so)
+                                  : static_cast<int64_t>(r) * so.b + static_cast<int64_t>(j) * so.h + at * so.t);
+    if (dtype == kBf16)
+        store4<Bf16>(out, off, x[0], x[1], x[2], x[3]);
+    else if (dtype == kF16)
+        store4<F16>(out, off, x[0], x[1], x[2], x[3]);
+    else
+        store4<F32>(out, off, x[0], x[1], x[2], x[3]);
+}
+
+struct BwdPlan {
+    AttnPlan q, kv;
+    int64_t pairs, bytes_delta, bytes_q, bytes_kv;
+};
+BwdPlan bwd_plan(const AttnArgs &a, int32_t dtype) {
+    const int64_t bn = dtype == kF32 ? 32 : 64;
+    BwdPlan p;
+    p.pairs = static_cast<int64_t>(a.n_kv) * a.Hk;
+    p.q = attn_plan(p.pairs, (static_cast<int64_t>(a.rows) + 127) / 128, (a.Lk + bn - 1) / bn, 4);
+    p.kv = attn_plan(p.pairs, (static_cast<int64_t>(a.Lk) + 127) / 128, (a.rows + bn - 1) / bn, 4);
+    p.bytes_delta = round16(p.pairs * a.rows * 4);
+    p.bytes_q = p.q.n_split > 1 ? p.q.n_split * p.pairs * a.rows * a.D * 4 : 0;
+    p.bytes_kv = p.kv.n_split > 1 ? 2 * p.kv.n_split * p.pairs * a.Lk * a.D * 4 : 0;
+    return p;
+}
+
+template <bool ROWS>
+hipError_t sum_splits(const AttnArgs &a, const float *part, void *out, const HeadStrides &so, int32_t dtype, int64_t n,
+                      hipStream_t stream) {
+    const int64_t total = static_cast<int64_t>(a.n_kv) * a.Hk * n * (a.D / 4);
+    return launch_slices((total + 255) / 256, 256, [&](int64_t first, uint32_t count) {
+        k_attn_sum<ROWS><<<count, 256, 0, stream>>>(a, part, out, so, dtype, total, first);
+    });
+}
+
+}  // namespace
+
+// delta, then the partial sums of dq, which those of dk and dv follow in time
+// and may overwrite.
+int64_t attn_bwd_workspace(const AttnArgs &a, int32_t dtype) {
+    const BwdPlan p = bwd_plan(a, dtype);
+    return p.bytes_delta + (p.bytes_q > p.bytes_kv ? p.bytes_q : p.bytes_kv);
+}
+
+hipError_t launch_attn_bwd(AttnArgs a, int32_t dtype, char *workspace, hipStream_t stream) {
+    const BwdPlan p = bwd_plan(a, dtype);
+    a.delta = reinterpret_cast<float *>(workspace);
+    a.part = reinterpret_cast<float *>(workspace + p.bytes_delta);
+    hipError_t e = hipSuccess;
+    a.n_tiles = fast_div(static_cast<uint32_t>(p.q.n_tiles));
+    a.n_split = fast_div(static_cast<uint32_t>(p.q.n_split));
+    a.split_tiles = static_cast<uint32_t>(p.q.split_tiles);
+    if (a.rows > 0) {
+        e = launch_slices(p.pairs * p.q.n_split * p.q.n_tiles, kAttnThreads, [&](int64_t first, uint32_t count) {
+            for_dtype_dim(dtype, a.D, [&](auto type, auto dim) {
+                using T = decltype(type);
+                constexpr int DP = decltype(dim)::value;
+                if (p.q.n_split > 1)
+                    k_attn_dq<T, DP, true><<<count, kAttnThreads, 0, stream>>>(a, first);
+                else
+                    k_attn_dq<T, DP, false><<<count, kAttnThreads, 0, stream>>>(a, first);
+            });
+        });
+        if (e == hipSuccess && p.q.n_split > 1) e = sum_splits<true>(a, a.part, a.dq, a.sdq, dtype, a.rows, stream);
+    }
+    if (e != hipSuccess || a.Lk == 0) return e;
+    a.n_tiles = fast_div(static_cast<uint32_t>(p.kv.n_tiles));
+    a.n_split = fast_div(static_cast<uint32_t>(p.kv.n_split));
+    a.split_tiles = static_cast<uint32_t>(p.kv.split_tiles);
+    e = launch_slices(p.pairs * p.kv.n_split * p.kv.n_tiles, kAttnThreads, [&](int64_t first, uint32_t count) {
+        for_dtype_dim(dtype, a.D, [&](auto type, auto dim) {
+            using T = decltype(type);
+            constexpr int DP = decltype(dim)::value;
+            if (p.kv.n_split > 1)
+                k_attn_dkv<T, DP, true><<<count, kAttnThreads, 0, stream>>>(a, first);
+            else
+                k_attn_dkv<T, DP, false><<<count, kAttnThreads, 0, stream>>>(a, first);
+        });
+    });
+    if (e != hipSuccess || p.kv.n_split == 1) return e;
+    const float *part_v = a.part + p.kv.n_split * p.pairs * a.Lk * a.D;
+    e = sum_splits<false>(a, a.part, a.dk, a.sdk, dtype, a.Lk, stream);
+    return e != hipSuccess ? e : sum_splits<false>(a, part_v, a.dv, a.sdv, dtype, a.Lk, stream);
+}
+
+}  // namespace pc

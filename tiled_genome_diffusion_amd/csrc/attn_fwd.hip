@@ -1,0 +1,247 @@
+// Cross attention, forward: O = softmax(scale Q K^T) V per key head of each
+// encoder state, over all query rows that share it (attn.hpp).
+#include "attn.hpp"
+#include "launch.hpp"
+
+namespace pc {
+namespace {
+
+// One workgroup: 4 wavefronts of 32 query rows each, one key head, one split
+// of the keys.  Keys and values pass through LDS in tiles of BN; each
+// wavefront forms S^T = K Q^T (keys x rows, so a row's scores lie in one lane
+// pair), keeps the running maximum m and sum l of the softmax per row, and
+// adds V^T P^T to O^T.  A single pass over the keys:
+//   m' = max(m, max S), O' = O 2^((m - m') c) + V^T P^T, P = 2^((S - m') c),
+// c = scale log2(e), all held in float32; P is rounded to the input type for
+// its product (as its other operand is), l sums the unrounded values.
+template <class T, int DP, bool SPLIT>
+__global__ __launch_bounds__(kAttnThreads) void k_attn_fwd(const AttnArgs a, int64_t block0) {
+    using TL = Tile<T, DP>;
+    __shared__ __align__(16) char s_k[2][TL::kBytes];
+    __shared__ __align__(16) char s_v[2][TL::kBytes];
+    const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
+    const int half = lane >> 5, col = lane & 31;
+    const uint32_t bid = static_cast<uint32_t>(block0) + xcd_remap(blockIdx.x, gridDim.x);
+    const uint32_t ps = div_by(bid, a.n_tiles), rt = bid - ps * a.n_tiles.d;
+    const uint32_t pair = div_by(ps, a.n_split), split = ps - pair * a.n_split.d;
+    const uint32_t r = div_by(pair, a.heads_kv), j = pair - r * a.heads_kv.d;
+
+    const uint32_t row = rt * (kAttnWaves * 32) + wave * 32 + col;
+    const bool row_ok = row < a.rows;
+    u32x4 qf[TL::FR];
+    {
+        const int64_t off = pair_offset(r, j, a, a.sq) + (row_ok ? row_offset(row, a, a.sq) : 0);
+#pragma unroll
+        for (int f = 0; f < TL::FR; ++f) qf[f] = load_chunk<T>(a.q, off, 2 * f + half, a.D, row_ok);
+    }
+    f32x16 o[TL::DT];
+#pragma unroll
+    for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+    float m = -INFINITY, l = 0.f;
+
+    const int n_keys = keys_of(r, a);
+    const int first = static_cast<int>(split * a.split_tiles) * TL::BN;
+    const int64_t span = static_cast<int64_t>(a.split_tiles) * TL::BN;
+    const int end = static_cast<int>(first + span < n_keys ? first + span : n_keys);
+    const int64_t koff = static_cast<int64_t>(r) * a.sk.b + static_cast<int64_t>(j) * a.sk.h;
+    const int64_t voff = static_cast<int64_t>(r) * a.sv.b + static_cast<int64_t>(j) * a.sv.h;
+
+    Staged<T, DP> gk, gv;
+    uint64_t valid = 0, seen = 0;
+    if (first < end) {
+        valid = valid_keys<TL::BN>(r, first, end, a);
+        gk.load_keys(a.k, koff, a.sk.t, first, valid, a.D);
+        gv.load_keys(a.v, voff, a.sv.t, first, valid, a.D);
+        gk.store(s_k[0]);
+        gv.store(s_v[0]);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int key0 = first; key0 < end; key0 += TL::BN, buf ^= 1) {
+        uint64_t next = 0;
+        const bool more = key0 + TL::BN < end;
+        if (more) {
+            next = valid_keys<TL::BN>(r, key0 + TL::BN, end, a);
+            gk.load_keys(a.k, koff, a.sk.t, key0 + TL::BN, next, a.D);
+            gv.load_keys(a.v, voff, a.sv.t, key0 + TL::BN, next, a.D);
+        }
+        seen |= valid;
+        if (valid != 0) {
+            f32x16 s[TL::SUB];
+#pragma unroll
+            for (int t = 0; t < TL::SUB; ++t) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[t][i] = 0.f;
+#pragma unroll
+                for (int f = 0; f < TL::FR; ++f) s[t] = mma<T>(TL::frag(s_k[buf], t * 32 + col, f, half), qf[f], s[t]);
+            }
+            if (valid != (TL::BN == 64 ? ~0ull : 0xFFFFFFFFull)) {
+#pragma unroll
+                for (int t = 0; t < TL::SUB; ++t) {
+                    const uint32_t bits = static_cast<uint32_t>(valid >> (32 * t)) >> (4 * half);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (!((bits >> (8 * (i / 4) + i % 4)) & 1)) s[t][i] = -INFINITY;
+                }
+            }
+            float top = s[0][0];
+#pragma unroll
+            for (int t = 0; t < TL::SUB; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
+            top = fmaxf(top, other_half(top));
+            const float m1 = fmaxf(m, top);
+            const float base = m1 == -INFINITY ? 0.f : m1 * a.scale_log2;  // all scores -inf so far: P = 0
+            const float fade = exp2_hw(fmaf(m, a.scale_log2, -base));
+            m = m1;
+            float sum = 0.f;
+#pragma unroll
+            for (int t = 0; t < TL::SUB; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s[t][i] = exp2_hw(fmaf(s[t][i], a.scale_log2, -base));
+                    sum += s[t][i];
+                }
+            l = fmaf(l, fade, sum);
+#pragma unroll
+            for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] *= fade;
+#pragma unroll
+            for (int t = 0; t < TL::SUB; ++t)
+#pragma unroll
+                for (int b = 0; b < TL::NB; ++b) {
+                    const u32x4 p = pack_frag<T>(s[t], b);
+#pragma unroll
+                    for (int d = 0; d < TL::DT; ++d)
+                        o[d] = mma<T>(TL::frag_t(s_v[buf], t * 32 + b * 2 * TL::EPC, d * 32, lane), p, o[d]);
+                }
+        }
+        if (more) {
+            gk.store(s_k[buf ^ 1]);
+            gv.store(s_v[buf ^ 1]);
+        }
+        valid = next;
+        __syncthreads();
+    }
+    l += other_half(l);
+    if (!row_ok) return;
+    if constexpr (SPLIT) {
+        const int64_t slot = (static_cast<int64_t>(split) * a.n_kv * a.Hk + pair) * a.rows + row;
+        float *part = a.part + slot * a.D;
+#pragma unroll
+        for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const int at = d * 32 + 2 * i + 4 * half;
+                if (at < a.D) *reinterpret_cast<f32v4 *>(part + at) = f32v4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+            }
+        if (half == 0) {
+            a.part_ml[2 * slot] = m;
+            a.part_ml[2 * slot + 1] = seen ? l : -1.f;  // -1: no attended key in this split
+        }
+        return;
+    }
+    // No attended key: zeros.  Attended keys whose scores are all -inf give l = 0 and NaN, as the softmax does.
+    const float inv = seen ? 1.f / l : 0.f;
+    const int64_t off = pair_offset(r, j, a, a.so) + row_offset(row, a, a.so);
+#pragma unroll
+    for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const int at = d * 32 + 2 * i + 4 * half;
+            if (at < a.D)
+                store4<T>(a.o, off + at, o[d][i] * inv, o[d][i + 1] * inv, o[d][i + 2] * inv, o[d][i + 3] * inv);
+        }
+    if (a.lse && half == 0) a.lse[lse_index(r, j, row, a)] = fmaf(m, a.scale, log2_hw(l) * kLn2);
+}
+
+// Joins the splits of a row: lane (row, 4 columns) weighs each split's partial
+// sum by 2^((m_s - m) c), in split order.
+__global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int32_t dtype, int64_t total, int64_t block0) {
+    const int64_t id = (block0 + blockIdx.x) * 256 + threadIdx.x;
+    if (id >= total) return;
+    const uint32_t quads = a.D / 4;
+    const int64_t slot0 = id / quads;  // pair * rows + row
+    const int d = static_cast<int>(id - slot0 * quads) * 4;
+    const uint32_t pair = static_cast<uint32_t>(slot0 / a.rows), row = static_cast<uint32_t>(slot0 - static_cast<int64_t>(pair) * a.rows);
+    const uint32_t r = pair / a.Hk, j = pair - r * a.Hk;
+    const int64_t step = static_cast<int64_t>(a.n_kv) * a.Hk * a.rows;
+    float m = -INFINITY;
+    bool seen = false;
+    for (uint32_t s = 0; s < a.n_split.d; ++s) {
+        const float ls = a.part_ml[2 * (slot0 + s * step) + 1];
+        if (ls == -1.f) continue;
+        seen = true;
+        m = fmaxf(m, a.part_ml[2 * (slot0 + s * step)]);
+    }
+    const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
+    float l = 0.f;
+    f32v4 o = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t s = 0; s < a.n_split.d; ++s) {
+        const int64_t slot = slot0 + s * step;
+        const float ls = a.part_ml[2 * slot + 1];
+        if (ls == -1.f) continue;
+        const float w = exp2_hw(fmaf(a.part_ml[2 * slot], a.scale_log2, -base));
+        l = fmaf(ls, w, l);
+        const f32v4 x = *reinterpret_cast<const f32v4 *>(a.part + slot * a.D + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = fmaf(x[i], w, o[i]);
+    }
+    const float inv = seen ? 1.f / l : 0.f;
+    const int64_t off = pair_offset(r, j, a, a.so) + row_offset(row, a, a.so) + d;
+    if (dtype == kBf16)
+        store4<Bf16>(a.o, off, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    else if (dtype == kF16)
+        store4<F16>(a.o, off, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    else
+        store4<F32>(a.o, off, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    if (a.lse && d == 0) a.lse[lse_index(r, j, row, a)] = fmaf(m, a.scale, log2_hw(l) * kLn2);
+}
+
+}  // namespace
+
+AttnPlan attn_fwd_plan(const AttnArgs &a, int32_t dtype) {
+    const int bn = dtype == kF32 ? 32 : 64;
+    return attn_plan(static_cast<int64_t>(a.n_kv) * a.Hk, (static_cast<int64_t>(a.rows) + 127) / 128,
+                     (a.Lk + bn - 1) / bn, 4);
+}
+
+int64_t attn_fwd_workspace(const AttnArgs &a, int32_t dtype) {
+    const AttnPlan p = attn_fwd_plan(a, dtype);
+    if (p.n_split == 1) return 0;
+    return round16(p.n_split * static_cast<int64_t>(a.n_kv) * a.Hk * a.rows * a.D * 4) +
+           round16(p.n_split * static_cast<int64_t>(a.n_kv) * a.Hk * a.rows * 8);
+}
+
+hipError_t launch_attn_fwd(AttnArgs a, int32_t dtype, char *workspace, hipStream_t stream) {
+    const AttnPlan p = attn_fwd_plan(a, dtype);
+    a.n_tiles = fast_div(static_cast<uint32_t>(p.n_tiles));
+    a.n_split = fast_div(static_cast<uint32_t>(p.n_split));
+    a.split_tiles = static_cast<uint32_t>(p.split_tiles);
+    const int64_t pairs = static_cast<int64_t>(a.n_kv) * a.Hk;
+    if (p.n_split > 1) {
+        a.part = reinterpret_cast<float *>(workspace);
+        a.part_ml = reinterpret_cast<float *>(workspace + round16(p.n_split * pairs * a.rows * a.D * 4));
+    }
+    const int64_t blocks = pairs * p.n_split * p.n_tiles;
+    const hipError_t e = launch_slices(blocks, kAttnThreads, [&](int64_t first, uint32_t count) {
+        for_dtype_dim(dtype, a.D, [&](auto type, auto dim) {
+            using T = decltype(type);
+            constexpr int DP = decltype(dim)::value;
+            if (p.n_split > 1)
+                k_attn_fwd<T, DP, true><<<count, kAttnThreads, 0, stream>>>(a, first);
+            else
+                k_attn_fwd<T, DP, false><<<count, kAttnThreads, 0, stream>>>(a, first);
+        });
+    });
+    if (e != hipSuccess || p.n_split == 1) return e;
+    const int64_t total = pairs * a.rows * (a.D / 4);
+    return launch_slices((total + 255) / 256, 256, [&](int64_t first, uint32_t count) {
+        k_attn_join<<<count, 256, 0, stream>>>(a, dtype, total, first);
+    });
+}
+
+}  // namespace pc

@@ -1,0 +1,294 @@
+// Root-mean-square norm of every query and key head, with its weight, and the
+// rotation of the head's pairs by the token's position, in one pass over the
+// data; and the gradients.
+//   n = x rstd w, rstd = (mean x^2 + eps)^(-1/2);
+//   pair i of the first 2 `half` values: (a, b) -> (a cos - b sin, b cos + a sin)
+// with angle = position * freq_i.  A pair is (i, i + half), or (2 i, 2 i + 1)
+// when interleaved.  Backward: g = the inverse rotation of dy,
+//   dw = sum over rows of g x rstd, h = g w,
+//   dx = rstd (h - x rstd mean(h x rstd)).
+//
+// Angles.  Each frequency arrives as turns per position in 64-bit fixed point,
+// so position times frequency modulo one turn is an integer product's low 64
+// bits: exact to 2^-64 turns per position for any 32-bit position, where a
+// float32 product would lose all digits of the angle at large positions.  The
+// top 32 bits as a float in [-1/2, 1/2) go to v_sin / v_cos, which take turns
+// (error <= 1.3e-7 of each, common.hpp).
+#include "launch.hpp"
+#include "norm_rope.hpp"
+
+namespace pc {
+namespace {
+
+constexpr int kNormThreads = 256;
+// cos and sin of a workgroup's tokens in LDS.
+constexpr int kTableBytes = 16384;
+
+// A head's row is held by LPR lanes of 16 bytes each, the lane's chunk the
+// same for every row it visits, so its weights stay in registers.
+template <class T, int LPR>
+struct RowLanes {
+    static constexpr int EPC = 16 / T::kSize;
+    static constexpr int kRows = kNormThreads / LPR;  // rows a workgroup holds at once
+
+    // Sum over the LPR lanes of a row (the same bits in each).
+    __device__ static __forceinline__ float sum(float v) {
+#pragma unroll
+        for (int m = 1; m < LPR; m <<= 1) v += __shfl_xor(v, m, 64);
+        return v;
+    }
+};
+
+// cos, sin of the tile's tokens: s_cs[token][pair].
+__device__ __forceinline__ void fill_table(const NormArgs &a, const NormSide &s, int64_t token0, int n_tokens,
+                                           float2 *s_cs) {
+    for (int id = static_cast<int>(threadIdx.x); id < n_tokens * a.half; id += kNormThreads) {
+        const int t = id / a.half, i = id - t * a.half;
+        const uint32_t token = static_cast<uint32_t>(token0 + t);
+        const uint32_t b = div_by(token, s.len), at = token - b * s.len.d;
+        const int64_t p = s.pos ? s.pos[static_cast<int64_t>(b) * s.pos_b + at] : static_cast<int64_t>(at);
+        const uint64_t turn = static_cast<uint64_t>(p) * a.turns[i];
+        const float rev = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-32f;
+        s_cs[id] = make_float2(__builtin_amdgcn_cosf(rev), __builtin_amdgcn_sinf(rev));
+    }
+}
+
+// The partner chunk of a half-split rotation, from the lane that holds it.
+template <int LPR>
+__device__ __forceinline__ u32x4 partner_chunk(u32x4 w, int src) {
+    u32x4 p;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = __shfl(w[j], src, 64);
+    return p;
+}
+
+// out = the rotation (sign +1) or inverse rotation (-1) of the lane's values
+// v; pv are the partner chunk's values (half-split pairs only).
+template <int EPC, bool INTER>
+__device__ __forceinline__ void rotate(const float (&v)[EPC], const float (&pv)[EPC], const float2 *cs, int e0,
+                                       int half, float sign, float (&out)[EPC]) {
+    if constexpr (INTER) {
+#pragma unroll
+        for (int i = 0; i < EPC; i += 2) {
+            const float2 t = cs[(e0 + i) >> 1];
+            const float sn = sign * t.y;
+            out[i] = fmaf(v[i], t.x, -(v[i + 1] * sn));
+            out[i + 1] = fmaf(v[i + 1], t.x, v[i] * sn);
+        }
+    } else {
+        const bool second = e0 >= half;
+        const int f = second ? e0 - half : e0;
+#pragma unroll
+        for (int i = 0; i < EPC; ++i) {
+            const float2 t = cs[f + i];
+            const float sn = second ? sign * t.y : -sign * t.y;
+            out[i] = fmaf(v[i], t.x, pv[i] * sn);
+        }
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store_chunk(void *base, int64_t element, const float (&x)[16 / T::kSize]) {
+    u32x4 w;
+    if constexpr (T::kSize == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(x[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack2<T>(x[2 * j], x[2 * j + 1]);
+    }
+    *reinterpret_cast<u32x4 *>(static_cast<char *>(base) + element * T::kSize) = w;
+}
+
+__device__ __forceinline__ int64_t head_offset(uint32_t token, uint32_t h, const NormSide &s, const HeadStrides &st) {
+    const uint32_t b = div_by(token, s.len), i = token - b * s.len.d;
+    return static_cast<int64_t>(b) * st.b + static_cast<int64_t>(i) * st.t + static_cast<int64_t>(h) * st.h;
+}
+
+// Forward and, with BWD, the gradients.  A workgroup takes tiles of `tile`
+// tokens, all heads of each; queries' workgroups come first in the grid.
+template <class T, int LPR, bool INTER, bool BWD>
+__global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, int64_t block0) {
+    using RL = RowLanes<T, LPR>;
+    constexpr int EPC = RL::EPC;
+    __shared__ __align__(16) float2 s_cs[kTableBytes / sizeof(float2)];
+    const uint32_t bid = static_cast<uint32_t>(block0) + blockIdx.x;
+    const int which = bid >= a.side[0].blocks ? 1 : 0;
+    const NormSide &s = a.side[which];
+    const uint32_t blk = which ? bid - a.side[0].blocks : bid;
+    const int tid = static_cast<int>(threadIdx.x);
+    const int c = tid % LPR, e0 = c * EPC;
+    const bool live = e0 < a.D;
+    const bool turned = live && e0 < 2 * a.half;
+    // the lane of the chunk half a rotated block away
+    const int lane = tid & 63, hc = a.half / EPC;
+    const int src = INTER || !turned ? lane : (c < hc ? lane + hc : lane - hc);
+    float w[EPC], pw[EPC], dw[EPC];
+#pragma unroll
+    for (int i = 0; i < EPC; ++i) {
+        w[i] = s.w && live ? s.w[e0 + i] : (live ? 1.f : 0.f);
+        pw[i] = !INTER && turned && s.w ? s.w[(c < hc ? e0 + a.half : e0 - a.half) + i] : 1.f;
+        dw[i] = 0.f;
+    }
+    for (uint32_t tile = blk; tile < s.tiles; tile += s.blocks) {
+        const int64_t token0 = static_cast<int64_t>(tile) * a.tile;
+        const int n_tokens = static_cast<int>(s.tokens - token0 < a.tile ? s.tokens - token0 : a.tile);
+        if (BWD) __syncthreads();  // the previous tile's table has been read
+        fill_table(a, s, token0, n_tokens, s_cs);
+        __syncthreads();
+        const int n_rows = n_tokens * static_cast<int>(s.heads.d);
+        for (int row0 = 0; row0 < n_rows; row0 += RL::kRows) {
+            const int row = row0 + tid / LPR;
+            const bool ok = live && row < n_rows;
+            const uint32_t t = div_by(static_cast<uint32_t>(row), s.heads), h = row - t * s.heads.d;
+            const uint32_t token = static_cast<uint32_t>(token0) + t;
+            const float2 *cs = s_cs + t * a.half;
+            u32x4 raw = {0u, 0u, 0u, 0u}, graw = {0u, 0u, 0u, 0u};
+            if (ok) {
+                raw = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(s.x) +
+                                                       (head_offset(token, h, s, s.sx) + e0) * T::kSize);
+                if (BWD)
+                    graw = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(s.dy) +
+                                                            (head_offset(token, h, s, s.sdy) + e0) * T::kSize);
+            }
+            float x[EPC];
+            unpack_chunk<T>(raw, x);
+            float q = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPC; ++i) q = fmaf(x[i], x[i], q);
+            const float rstd = 1.f / sqrtf(fmaf(RL::sum(q), a.inv_d, a.eps));
+            if constexpr (!BWD) {
+                float n[EPC], pn[EPC], y[EPC];
+                if constexpr (!INTER) unpack_chunk<T>(partner_chunk<LPR>(raw, src), pn);
+#pragma unroll
+                for (int i = 0; i < EPC; ++i) {
+                    y[i] = n[i] = x[i] * rstd * w[i];
+                    if constexpr (!INTER) pn[i] = pn[i] * rstd * pw[i];
+                }
+                if (turned && ok) rotate<EPC, INTER>(n, pn, cs, e0, a.half, 1.f, y);
+                if (ok) store_chunk<T>(s.y, head_offset(token, h, s, s.sy) + e0, y);
+            } else {
+                float g[EPC], pg[EPC], u[EPC];
+                unpack_chunk<T>(graw, g);
+                if constexpr (!INTER) unpack_chunk<T>(partner_chunk<LPR>(graw, src), pg);
+#pragma unroll
+                for (int i = 0; i < EPC; ++i) u[i] = g[i];
+                if (turned && ok) rotate<EPC, INTER>(g, pg, cs, e0, a.half, -1.f, u);
+                float dot = 0.f;
+#pragma unroll
+                for (int i = 0; i < EPC; ++i) {
+                    x[i] *= rstd;
+                    dw[i] = fmaf(u[i], x[i], dw[i]);
+                    u[i] *= w[i];
+                    dot = fmaf(u[i], x[i], dot);
+                }
+                const float mean = RL::sum(dot) * a.inv_d;
+#pragma unroll
+                for (int i = 0; i < EPC; ++i) u[i] = rstd * fmaf(-mean, x[i], u[i]);
+                if (ok) store_chunk<T>(s.dx, head_offset(token, h, s, s.sdx) + e0, u);
+            }
+        }
+    }
+    if constexpr (BWD) {
+        if (!s.dw) return;
+        // Sum of the workgroup's row groups, in their order.
+        __syncthreads();
+        float *sum = reinterpret_cast<float *>(s_cs);  // [kRows][LPR * EPC] at most 8 KB
+#pragma unroll
+        for (int i = 0; i < EPC; ++i) sum[(tid / LPR) * (LPR * EPC) + e0 + i] = dw[i];
+        __syncthreads();
+        if (tid < a.D) {
+            float v = 0.f;
+            for (int g = 0; g < RL::kRows; ++g) v += sum[g * (LPR * EPC) + tid];
+            s.part[static_cast<int64_t>(blk) * a.D + tid] = v;
+        }
+    }
+}
+
+// dw = sum of the workgroups' partial sums: lane (d, g) adds every 8th of them
+// in order, then the eight are added in order.  Workgroup 0: queries, 1: keys.
+__global__ __launch_bounds__(1024) void k_norm_dw(const NormArgs a, int64_t block0) {
+    __shared__ float s_sum[8][128];
+    const NormSide &s = a.side[block0 + blockIdx.x];
+    if (!s.dw) return;
+    const int d = static_cast<int>(threadIdx.x) & 127, g = static_cast<int>(threadIdx.x) >> 7;
+    float v = 0.f;
+    if (d < a.D)
+        for (uint32_t b = g; b < s.blocks; b += 8) v += s.part[static_cast<int64_t>(b) * a.D + d];
+    s_sum[g][d] = v;
+    __syncthreads();
+    if (g == 0 && d < a.D) {
+        for (int i = 1; i < 8; ++i) v += s_sum[i][d];
+        s.dw[d] = v;
+    }
+}
+
+constexpr uint32_t kBwdBlocks = 1024;  // of a side: its tiles are dealt to at most this many workgroups
+
+// Tokens per tile: about 8 KB of rows, as many as the table holds.
+void plan(NormArgs &a, int32_t dtype, bool bwd) {
+    const uint32_t size = dtype == kF32 ? 4 : 2;
+    const uint32_t heads = a.side[0].tokens ? a.side[0].heads.d : a.side[1].heads.d;
+    uint32_t tile = 16384u / (static_cast<uint32_t>(a.D) * size * heads);
+    const uint32_t most = a.half > 0 ? kTableBytes / (8u * a.half) : 64u;
+    tile = tile < 1 ? 1 : tile;
+    a.tile = tile > most ? most : tile;
+    for (NormSide &s : a.side) {
+        s.tiles = static_cast<uint32_t>((s.tokens + a.tile - 1) / a.tile);
+        s.blocks = bwd && s.tiles > kBwdBlocks ? kBwdBlocks : s.tiles;
+    }
+}
+
+template <class F>
+void for_row_lanes(int32_t dtype, int32_t dim, bool interleaved, F &&f) {
+    const auto inter = [&](auto type, auto lanes) {
+        if (interleaved) f(type, lanes, std::integral_constant<bool, true>{});
+        else f(type, lanes, std::integral_constant<bool, false>{});
+    };
+    const auto lanes = [&](auto type) {
+        const int n = dim * decltype(type)::kSize / 16;
+        if (n <= 4) inter(type, std::integral_constant<int, 4>{});
+        else if (n <= 8) inter(type, std::integral_constant<int, 8>{});
+        else if (n <= 16) inter(type, std::integral_constant<int, 16>{});
+        else inter(type, std::integral_constant<int, 32>{});
+    };
+    if (dtype == kBf16) lanes(Bf16{});
+    else if (dtype == kF16) lanes(F16{});
+    else lanes(F32{});
+}
+
+template <bool BWD>
+hipError_t launch(const NormArgs &a, int32_t dtype, bool interleaved, hipStream_t stream) {
+    const int64_t blocks = static_cast<int64_t>(a.side[0].blocks) + a.side[1].blocks;
+    return launch_slices(blocks, kNormThreads, [&](int64_t first, uint32_t count) {
+        for_row_lanes(dtype, a.D, interleaved, [&](auto type, auto lanes, auto inter) {
+            k_norm_rope<decltype(type), decltype(lanes)::value, decltype(inter)::value, BWD>
+                <<<count, kNormThreads, 0, stream>>>(a, first);
+        });
+    });
+}
+
+}  // namespace
+
+hipError_t launch_norm_fwd(NormArgs &a, int32_t dtype, bool interleaved, hipStream_t stream) {
+    plan(a, dtype, false);
+    return launch<false>(a, dtype, interleaved, stream);
+}
+
+int64_t norm_bwd_workspace(NormArgs &a, int32_t dtype) {
+    plan(a, dtype, true);
+    return round16((static_cast<int64_t>(a.side[0].blocks) + a.side[1].blocks) * a.D * 4);
+}
+
+hipError_t launch_norm_bwd(NormArgs &a, int32_t dtype, bool interleaved, char *workspace, hipStream_t stream) {
+    plan(a, dtype, true);
+    a.side[0].part = reinterpret_cast<float *>(workspace);
+    a.side[1].part = a.side[0].part + static_cast<int64_t>(a.side[0].blocks) * a.D;
+    const hipError_t e = launch<true>(a, dtype, interleaved, stream);
+    if (e != hipSuccess || (!a.side[0].dw && !a.side[1].dw)) return e;
+    return launch_slices(2, 1024, [&](int64_t first, uint32_t count) {
+        k_norm_dw<<<count, 1024, 0, stream>>>(a, first);
+    });
+}
+
+}  // namespace pc
