@@ -13,7 +13,7 @@ namespace {
 // dQ (and delta, for the kernel below): 4 wavefronts of 32 rows, keys and
 // values in LDS tiles, as the forward.
 template <class T, int DP, bool SPLIT>
-__global__ __launch_bounds__(kAttnThreads) void k_attn_dq(const AttnArgs a, int64_t block0) {
+__global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k_attn_dq(const AttnArgs a, int64_t block0) {
     using TL = Tile<T, DP>;
     __shared__ __align__(16) char s_k[2][TL::kBytes];
     __shared__ __align__(16) char s_v[2][TL::kBytes];
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_dq(const AttnArgs a, int6
 // is a lane and P and dS are the second operands of dV^T = dO^T P and
 // dK^T = Q^T dS as they stand.
 template <class T, int DP, bool SPLIT>
-__global__ __launch_bounds__(kAttnThreads) void k_attn_dkv(const AttnArgs a, int64_t block0) {
+__global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k_attn_dkv(const AttnArgs a, int64_t block0) {
     using TL = Tile<T, DP>;
     __shared__ __align__(16) char s_q[2][TL::kBytes];
     __shared__ __align__(16) char s_g[2][TL::kBytes];

@@ -6,16 +6,23 @@
 namespace pc {
 namespace {
 
-// One workgroup: 4 wavefronts of 32 query rows each, one key head, one split
-// of the keys.  Keys and values pass through LDS in tiles of BN; each
-// wavefront forms S^T = K Q^T (keys x rows, so a row's scores lie in one lane
-// pair), keeps the running maximum m and sum l of the softmax per row, and
-// adds V^T P^T to O^T.  A single pass over the keys:
-//   m' = max(m, max S), O' = O 2^((m - m') c) + V^T P^T, P = 2^((S - m') c),
-// c = scale log2(e), all held in float32; P is rounded to the input type for
-// its product (as its other operand is), l sums the unrounded values.
-template <class T, int DP, bool SPLIT>
-__global__ __launch_bounds__(kAttnThreads) void k_attn_fwd(const AttnArgs a, int64_t block0) {
+// One workgroup: 4 wavefronts of NR blocks of 32 query rows each, one key
+// head, one split of the keys.  Keys and values pass through LDS in tiles of
+// BN; each wavefront forms S^T = K Q^T (keys x rows, so a row's scores lie in
+// one lane pair), keeps the running maximum and sum of the softmax per row,
+// and adds V^T P^T to O^T.  A single pass over the keys, with P relative to a
+// base m of the row:
+//   P = 2^((S - m) c), l += sum P, O^T += V^T P^T,   c = scale log2(e),
+// all in float32; P is rounded to the input type for its product (as that
+// product's other operand is), l sums the unrounded values.  When a row's
+// maximum has outgrown its base by more than 2^kSlack in P, every row of the
+// wavefront takes its maximum as its base and l and O are scaled to it; P
+// stays below 2^kSlack, so neither float32 nor float16 can overflow, and the
+// scaling of O (one instruction per score at dim 64) is rare.
+constexpr float kSlack = 8.f;
+
+template <class T, int DP, int NR, bool SPLIT>
+__global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k_attn_fwd(const AttnArgs a, int64_t block0) {
     using TL = Tile<T, DP>;
     __shared__ __align__(16) char s_k[2][TL::kBytes];
     __shared__ __align__(16) char s_v[2][TL::kBytes];
@@ -26,20 +33,24 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_fwd(const AttnArgs a, int
     const uint32_t pair = div_by(ps, a.n_split), split = ps - pair * a.n_split.d;
     const uint32_t r = div_by(pair, a.heads_kv), j = pair - r * a.heads_kv.d;
 
-    const uint32_t row = rt * (kAttnWaves * 32) + wave * 32 + col;
-    const bool row_ok = row < a.rows;
-    u32x4 qf[TL::FR];
-    {
-        const int64_t off = pair_offset(r, j, a, a.sq) + (row_ok ? row_offset(row, a, a.sq) : 0);
+    const uint32_t row0 = (rt * kAttnWaves + wave) * (NR * 32) + col;  // and row0 + 32
+    u32x4 qf[NR][TL::FR];
+    f32x16 o[NR][TL::DT];
+    float m[NR], l[NR];
 #pragma unroll
-        for (int f = 0; f < TL::FR; ++f) qf[f] = load_chunk<T>(a.q, off, 2 * f + half, a.D, row_ok);
+    for (int n = 0; n < NR; ++n) {
+        const uint32_t row = row0 + 32 * n;
+        const bool ok = row < a.rows;
+        const int64_t off = pair_offset(r, j, a, a.sq) + (ok ? row_offset(row, a, a.sq) : 0);
+#pragma unroll
+        for (int f = 0; f < TL::FR; ++f) qf[n][f] = load_chunk<T>(a.q, off, 2 * f + half, a.D, ok);
+#pragma unroll
+        for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[n][d][i] = 0.f;
+        m[n] = -INFINITY;
+        l[n] = 0.f;
     }
-    f32x16 o[TL::DT];
-#pragma unroll
-    for (int d = 0; d < TL::DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-    float m = -INFINITY, l = 0.f;
 
     const int n_keys = keys_of(r, a);
     const int first = static_cast<int>(split * a.split_tiles) * TL::BN;
@@ -69,13 +80,19 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_fwd(const AttnArgs a, int
         }
         seen |= valid;
         if (valid != 0) {
-            f32x16 s[TL::SUB];
+            f32x16 s[NR][TL::SUB];
 #pragma unroll
             for (int t = 0; t < TL::SUB; ++t) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[t][i] = 0.f;
+                for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int f = 0; f < TL::FR; ++f) s[t] = mma<T>(TL::frag(s_k[buf], t * 32 + col, f, half), qf[f], s[t]);
+                    for (int i = 0; i < 16; ++i) s[n][t][i] = 0.f;
+#pragma unroll
+                for (int f = 0; f < TL::FR; ++f) {
+                    const u32x4 kf = TL::frag(s_k[buf], t * 32 + col, f, half);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) s[n][t] = mma<T>(kf, qf[n][f], s[n][t]);
+                }
             }
             if (valid != (TL::BN == 64 ? ~0ull : 0xFFFFFFFFull)) {
 #pragma unroll
@@ -83,40 +100,63 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_fwd(const AttnArgs a, int
                     const uint32_t bits = static_cast<uint32_t>(valid >> (32 * t)) >> (4 * half);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (!((bits >> (8 * (i / 4) + i % 4)) & 1)) s[t][i] = -INFINITY;
+                        if (!((bits >> (8 * (i / 4) + i % 4)) & 1))
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) s[n][t][i] = -INFINITY;
                 }
             }
-            float top = s[0][0];
+            float top[NR];
+            bool grown = false;
 #pragma unroll
-            for (int t = 0; t < TL::SUB; ++t)
+            for (int n = 0; n < NR; ++n) {
+                top[n] = s[n][0][0];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-            top = fmaxf(top, other_half(top));
-            const float m1 = fmaxf(m, top);
-            const float base = m1 == -INFINITY ? 0.f : m1 * a.scale_log2;  // all scores -inf so far: P = 0
-            const float fade = exp2_hw(fmaf(m, a.scale_log2, -base));
-            m = m1;
-            float sum = 0.f;
+                for (int t = 0; t < TL::SUB; ++t)
 #pragma unroll
-            for (int t = 0; t < TL::SUB; ++t)
+                    for (int i = 0; i < 16; ++i) top[n] = fmaxf(top[n], s[n][t][i]);
+                top[n] = fmaxf(top[n], other_half(top[n]));
+                // m is -inf until a score is not: then any such score has outgrown it
+                grown |= (top[n] - m[n]) * a.scale_log2 > kSlack;
+            }
+            if (__any(grown)) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[t][i] = exp2_hw(fmaf(s[t][i], a.scale_log2, -base));
-                    sum += s[t][i];
+                for (int n = 0; n < NR; ++n) {
+                    const float m1 = fmaxf(m[n], top[n]);
+                    const float fade = m1 == m[n] ? 1.f : exp2_hw((m[n] - m1) * a.scale_log2);
+                    m[n] = m1;
+                    l[n] *= fade;
+#pragma unroll
+                    for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[n][d][i] *= fade;
                 }
-            l = fmaf(l, fade, sum);
+            }
 #pragma unroll
-            for (int d = 0; d < TL::DT; ++d)
+            for (int n = 0; n < NR; ++n) {
+                const float base = m[n] == -INFINITY ? 0.f : m[n] * a.scale_log2;  // all scores -inf so far: P = 0
+                float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[d][i] *= fade;
+                for (int t = 0; t < TL::SUB; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        s[n][t][i] = exp2_hw(fmaf(s[n][t][i], a.scale_log2, -base));
+                        sum += s[n][t][i];
+                    }
+                l[n] += sum;
+            }
 #pragma unroll
             for (int t = 0; t < TL::SUB; ++t)
 #pragma unroll
                 for (int b = 0; b < TL::NB; ++b) {
-                    const u32x4 p = pack_frag<T>(s[t], b);
+                    u32x4 p[NR];
 #pragma unroll
-                    for (int d = 0; d < TL::DT; ++d)
-                        o[d] = mma<T>(TL::frag_t(s_v[buf], t * 32 + b * 2 * TL::EPC, d * 32, lane), p, o[d]);
+                    for (int n = 0; n < NR; ++n) p[n] = pack_frag<T>(s[n][t], b);
+#pragma unroll
+                    for (int d = 0; d < TL::DT; ++d) {
+                        const u32x4 vf = TL::frag_t(s_v[buf], t * 32 + b * 2 * TL::EPC, d * 32, lane);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) o[n][d] = mma<T>(vf, p[n], o[n][d]);
+                    }
                 }
         }
         if (more) {
@@ -126,36 +166,43 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_fwd(const AttnArgs a, int
         valid = next;
         __syncthreads();
     }
-    l += other_half(l);
-    if (!row_ok) return;
-    if constexpr (SPLIT) {
-        const int64_t slot = (static_cast<int64_t>(split) * a.n_kv * a.Hk + pair) * a.rows + row;
-        float *part = a.part + slot * a.D;
 #pragma unroll
-        for (int d = 0; d < TL::DT; ++d)
+    for (int n = 0; n < NR; ++n) {
+        const float total = l[n] + other_half(l[n]);
+        const uint32_t row = row0 + 32 * n;
+        if (row >= a.rows) continue;
+        if constexpr (SPLIT) {
+            const int64_t slot = (static_cast<int64_t>(split) * a.n_kv * a.Hk + pair) * a.rows + row;
+            float *part = a.part + slot * a.D;
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const int at = d * 32 + 2 * i + 4 * half;
-                if (at < a.D) *reinterpret_cast<f32v4 *>(part + at) = f32v4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+            for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const int at = d * 32 + 2 * i + 4 * half;
+                    if (at < a.D)
+                        *reinterpret_cast<f32v4 *>(part + at) =
+                            f32v4{o[n][d][i], o[n][d][i + 1], o[n][d][i + 2], o[n][d][i + 3]};
+                }
+            if (half == 0) {
+                a.part_ml[2 * slot] = m[n];
+                a.part_ml[2 * slot + 1] = seen ? total : -1.f;  // -1: no attended key in this split
             }
-        if (half == 0) {
-            a.part_ml[2 * slot] = m;
-            a.part_ml[2 * slot + 1] = seen ? l : -1.f;  // -1: no attended key in this split
+        } else {
+            // No attended key: zeros.  Attended keys whose scores are all -inf give l = 0 and NaN, as the softmax does.
+            const float inv = seen ? 1.f / total : 0.f;
+            const int64_t off = pair_offset(r, j, a, a.so) + row_offset(row, a, a.so);
+#pragma unroll
+            for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const int at = d * 32 + 2 * i + 4 * half;
+                    if (at < a.D)
+                        store4<T>(a.o, off + at, o[n][d][i] * inv, o[n][d][i + 1] * inv, o[n][d][i + 2] * inv,
+                                  o[n][d][i + 3] * inv);
+                }
+            if (a.lse && half == 0) a.lse[lse_index(r, j, row, a)] = fmaf(m[n], a.scale, log2_hw(total) * kLn2);
         }
-        return;
     }
-    // No attended key: zeros.  Attended keys whose scores are all -inf give l = 0 and NaN, as the softmax does.
-    const float inv = seen ? 1.f / l : 0.f;
-    const int64_t off = pair_offset(r, j, a, a.so) + row_offset(row, a, a.so);
-#pragma unroll
-    for (int d = 0; d < TL::DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            const int at = d * 32 + 2 * i + 4 * half;
-            if (at < a.D)
-                store4<T>(a.o, off + at, o[d][i] * inv, o[d][i + 1] * inv, o[d][i + 2] * inv, o[d][i + 3] * inv);
-        }
-    if (a.lse && half == 0) a.lse[lse_index(r, j, row, a)] = fmaf(m, a.scale, log2_hw(l) * kLn2);
 }
 
 // Joins the splits of a row: lane (row, 4 columns) weighs each split's partial
@@ -203,10 +250,17 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int32_t dty
 
 }  // namespace
 
+// Row blocks of a wavefront: two where that still leaves two workgroups per
+// compute unit (each K and V fragment read from LDS then serves two products).
+int row_blocks(const AttnArgs &a, int32_t dtype) {
+    const int64_t pairs = static_cast<int64_t>(a.n_kv) * a.Hk;
+    return dtype != kF32 && a.D <= 64 && pairs * ((static_cast<int64_t>(a.rows) + 255) / 256) >= 512 ? 2 : 1;
+}
+
 AttnPlan attn_fwd_plan(const AttnArgs &a, int32_t dtype) {
     const int bn = dtype == kF32 ? 32 : 64;
-    return attn_plan(static_cast<int64_t>(a.n_kv) * a.Hk, (static_cast<int64_t>(a.rows) + 127) / 128,
-                     (a.Lk + bn - 1) / bn, 4);
+    const int64_t rows = 128 * row_blocks(a, dtype);
+    return attn_plan(static_cast<int64_t>(a.n_kv) * a.Hk, (a.rows + rows - 1) / rows, (a.Lk + bn - 1) / bn, 4);
 }
 
 int64_t attn_fwd_workspace(const AttnArgs &a, int32_t dtype) {
@@ -227,14 +281,18 @@ hipError_t launch_attn_fwd(AttnArgs a, int32_t dtype, char *workspace, hipStream
         a.part_ml = reinterpret_cast<float *>(workspace + round16(p.n_split * pairs * a.rows * a.D * 4));
     }
     const int64_t blocks = pairs * p.n_split * p.n_tiles;
+    const int nr = row_blocks(a, dtype);
     const hipError_t e = launch_slices(blocks, kAttnThreads, [&](int64_t first, uint32_t count) {
         for_dtype_dim(dtype, a.D, [&](auto type, auto dim) {
             using T = decltype(type);
             constexpr int DP = decltype(dim)::value;
+            if constexpr (T::kSize == 2 && DP <= 64) {
+                if (nr == 2) return k_attn_fwd<T, DP, 2, false><<<count, kAttnThreads, 0, stream>>>(a, first);
+            }
             if (p.n_split > 1)
-                k_attn_fwd<T, DP, true><<<count, kAttnThreads, 0, stream>>>(a, first);
+                k_attn_fwd<T, DP, 1, true><<<count, kAttnThreads, 0, stream>>>(a, first);
             else
-                k_attn_fwd<T, DP, false><<<count, kAttnThreads, 0, stream>>>(a, first);
+                k_attn_fwd<T, DP, 1, false><<<count, kAttnThreads, 0, stream>>>(a, first);
         });
     });
     if (e != hipSuccess || p.n_split == 1) return e;

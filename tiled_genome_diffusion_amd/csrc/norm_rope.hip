@@ -249,8 +249,8 @@ void for_row_lanes(int32_t dtype, int32_t dim, bool interleaved, F &&f) {
         const int n = dim * decltype(type)::kSize / 16;
         if (n <= 4) inter(type, std::integral_constant<int, 4>{});
         else if (n <= 8) inter(type, std::integral_constant<int, 8>{});
-        else if (n <= 16) inter(type, std::integral_constant<int, 16>{});
-        else inter(type, std::integral_constant<int, 32>{});
+        else if (decltype(type)::kSize == 2 || n <= 16) inter(type, std::integral_constant<int, 16>{});
+        else if constexpr (decltype(type)::kSize == 4) inter(type, std::integral_constant<int, 32>{});
     };
     if (dtype == kBf16) lanes(Bf16{});
     else if (dtype == kF16) lanes(F16{});
