@@ -254,32 +254,102 @@ __device__ __forceinline__ u32x4 load_chunk(const void *base, int64_t row, int c
     return w;
 }
 
-// The chunks of one tile that this lane stages, held in registers between the
-// global loads and the LDS stores.
+// 16 bytes per lane from global memory straight into LDS: lane l's go to
+// lds + 16 l (`lds` is the same in every lane of the wavefront); lanes that are
+// off leave their place as it is.  Counted by vmcnt: wait_loads() before the
+// barrier that hands the tile over.
+__device__ __forceinline__ void load_to_lds(const char *global, char *lds) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)global,
+                                     (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+
+// One workgroup's staging of a tile: each lane brings NCH chunks.  LDS places
+// are in lane order, so the permutation of the chunks is applied to the global
+// address.  Places that are not loaded (rows past the end, keys that are not
+// attended, chunks past the head's size) keep what they held: zero, or a value
+// of an earlier tile of the same sequence, which only meets factors of zero.
 template <class T, int DP>
-struct Staged {
+struct Loader {
     using TL = Tile<T, DP>;
-    u32x4 w[TL::NCH];
-    __device__ __forceinline__ void store(char *tile) const {
-#pragma unroll
-        for (int i = 0; i < TL::NCH; ++i) {
-            const int id = static_cast<int>(threadIdx.x) + i * kAttnThreads;
-            *reinterpret_cast<u32x4 *>(tile + TL::at(id / TL::CH, id % TL::CH)) = w[i];
-        }
+    const char *p[TL::NCH];
+    uint32_t live;  // bit i: chunk i lies within the head
+    bool whole;     // every chunk does
+
+    __device__ static __forceinline__ int row(int i) { return (static_cast<int>(threadIdx.x) + i * kAttnThreads) / TL::CH; }
+    __device__ static __forceinline__ int chunk(int i) {
+        const int id = static_cast<int>(threadIdx.x) + i * kAttnThreads;
+        return TL::swz(id / TL::CH, id % TL::CH);
     }
-    // Rows row0 .. row0 + BN - 1 of keys or values; those whose bit of `valid`
-    // is clear read as zero, so nothing an unattended place holds (NaN, too)
-    // reaches a product.
-    __device__ __forceinline__ void load_keys(const void *base, int64_t off, int64_t stride, int row0, uint64_t valid,
-                                              int dim) {
+    __device__ __forceinline__ void init(int dim) {
+        live = 0;
+        whole = dim == DP;
 #pragma unroll
-        for (int i = 0; i < TL::NCH; ++i) {
-            const int id = static_cast<int>(threadIdx.x) + i * kAttnThreads;
-            const int r = id / TL::CH;
-            w[i] = load_chunk<T>(base, off + (row0 + r) * stride, id % TL::CH, dim, (valid >> r) & 1);
+        for (int i = 0; i < TL::NCH; ++i)
+            if (chunk(i) * TL::EPC < dim) live |= 1u << i;
+    }
+    // Rows row0, row0 + 1, ... at `stride` elements.
+    __device__ __forceinline__ void point(const void *base, int64_t off, int64_t stride, int64_t row0) {
+#pragma unroll
+        for (int i = 0; i < TL::NCH; ++i)
+            p[i] = static_cast<const char *>(base) + (off + (row0 + row(i)) * stride + chunk(i) * TL::EPC) * TL::kSize;
+    }
+    __device__ __forceinline__ void advance(int64_t bytes) {
+#pragma unroll
+        for (int i = 0; i < TL::NCH; ++i) p[i] += bytes;
+    }
+    // Starts the loads of the rows whose bit of `valid` is set (all: every bit of the tile is).
+    __device__ __forceinline__ void start(char *tile, uint64_t valid, bool all) const {
+        char *at = tile + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * 1024;
+        if (all && whole) {
+#pragma unroll
+            for (int i = 0; i < TL::NCH; ++i) load_to_lds(p[i], at + i * (kAttnThreads * 16));
+        } else {
+#pragma unroll
+            for (int i = 0; i < TL::NCH; ++i)
+                if (((valid >> row(i)) & (live >> i)) & 1) load_to_lds(p[i], at + i * (kAttnThreads * 16));
         }
     }
 };
+template <int BYTES>
+__device__ __forceinline__ void zero_lds(char *lds) {
+#pragma unroll
+    for (int i = 0; i < BYTES; i += kAttnThreads * 16)
+        *reinterpret_cast<u32x4 *>(lds + i + static_cast<int>(threadIdx.x) * 16) = u32x4{0u, 0u, 0u, 0u};
+}
+
+// Four accumulator quads of a row block (columns d0 .. d0 + 31 of one row, in
+// the order the accumulator holds them), rounded and stored: with 16-bit types
+// the halves of a row's lane pair exchange quads first, so that each stores 16
+// bytes.  Columns from `dim` on are left out; `ok`: the row exists.
+template <class T>
+__device__ __forceinline__ void store_row_block(void *base, int64_t off, const f32x16 &x, float f, int d0, int half,
+                                                int dim, bool ok) {
+    if constexpr (T::kSize == 4) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int at = d0 + 8 * g + 4 * half;
+            if (ok && at < dim)
+                *reinterpret_cast<f32v4 *>(static_cast<float *>(base) + off + at) =
+                    f32v4{x[4 * g] * f, x[4 * g + 1] * f, x[4 * g + 2] * f, x[4 * g + 3] * f};
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+            u32x4 w;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const u32x2 r = __builtin_amdgcn_permlane32_swap(pack2<T>(x[4 * g + 2 * j] * f, x[4 * g + 2 * j + 1] * f),
+                                                                 pack2<T>(x[4 * g + 4 + 2 * j] * f, x[4 * g + 5 + 2 * j] * f),
+                                                                 false, false);
+                w[j] = r.x;      // values 0..3 of group g (half 0) or g + 1 (half 1)
+                w[2 + j] = r.y;  // values 4..7
+            }
+            const int at = d0 + 8 * (g + half);
+            if (ok && at < dim) *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(base) + off + at) = w;
+        }
+    }
+}
 
 // Element offset of query row `row` of (state r, key head j), without the
 // batch and head offsets of (r, j) itself.

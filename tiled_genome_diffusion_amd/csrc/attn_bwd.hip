@@ -15,8 +15,7 @@ namespace {
 template <class T, int DP, bool SPLIT>
 __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k_attn_dq(const AttnArgs a, int64_t block0) {
     using TL = Tile<T, DP>;
-    __shared__ __align__(16) char s_k[2][TL::kBytes];
-    __shared__ __align__(16) char s_v[2][TL::kBytes];
+    __shared__ __align__(16) char s_kv[2][2 * TL::kBytes];
     const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
     const int half = lane >> 5, col = lane & 31;
     const uint32_t bid = static_cast<uint32_t>(block0) + xcd_remap(blockIdx.x, gridDim.x);
@@ -59,24 +58,35 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
     const int64_t koff = static_cast<int64_t>(r) * a.sk.b + static_cast<int64_t>(j) * a.sk.h;
     const int64_t voff = static_cast<int64_t>(r) * a.sv.b + static_cast<int64_t>(j) * a.sv.h;
 
-    Staged<T, DP> gk, gv;
+    constexpr uint64_t kAll = TL::BN == 64 ? ~0ull : 0xFFFFFFFFull;
+    Loader<T, DP> gk, gv;
     uint64_t valid = 0;
     if (first < end) {
+        if (a.D < DP || a.key_mask || (end - first) % TL::BN != 0) {
+            zero_lds<4 * TL::kBytes>(s_kv[0]);
+            __syncthreads();
+        }
+        gk.init(a.D);
+        gv.init(a.D);
+        gk.point(a.k, koff, a.sk.t, first);
+        gv.point(a.v, voff, a.sv.t, first);
         valid = valid_keys<TL::BN>(r, first, end, a);
-        gk.load_keys(a.k, koff, a.sk.t, first, valid, a.D);
-        gv.load_keys(a.v, voff, a.sv.t, first, valid, a.D);
-        gk.store(s_k[0]);
-        gv.store(s_v[0]);
+        gk.start(s_kv[0], valid, valid == kAll);
+        gv.start(s_kv[0] + TL::kBytes, valid, valid == kAll);
     }
-    __syncthreads();
+    const int64_t kstep = a.sk.t * (TL::BN * T::kSize), vstep = a.sv.t * (TL::BN * T::kSize);
     int buf = 0;
     for (int key0 = first; key0 < end; key0 += TL::BN, buf ^= 1) {
+        wait_loads();
+        __syncthreads();  // the tile is here, and every wavefront has left the other one
+        const char *s_k = s_kv[buf], *s_v = s_kv[buf] + TL::kBytes;
         uint64_t next = 0;
-        const bool more = key0 + TL::BN < end;
-        if (more) {
+        if (key0 + TL::BN < end) {
+            gk.advance(kstep);
+            gv.advance(vstep);
             next = valid_keys<TL::BN>(r, key0 + TL::BN, end, a);
-            gk.load_keys(a.k, koff, a.sk.t, key0 + TL::BN, next, a.D);
-            gv.load_keys(a.v, voff, a.sv.t, key0 + TL::BN, next, a.D);
+            gk.start(s_kv[buf ^ 1], next, next == kAll);
+            gv.start(s_kv[buf ^ 1] + TL::kBytes, next, next == kAll);
         }
 #pragma unroll
         for (int t = 0; t < TL::SUB; ++t) {
@@ -87,8 +97,8 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
             for (int i = 0; i < 16; ++i) s[i] = g[i] = 0.f;
 #pragma unroll
             for (int f = 0; f < TL::FR; ++f) {
-                s = mma<T>(TL::frag(s_k[buf], t * 32 + col, f, half), qf[f], s);
-                g = mma<T>(TL::frag(s_v[buf], t * 32 + col, f, half), gf[f], g);
+                s = mma<T>(TL::frag(s_k, t * 32 + col, f, half), qf[f], s);
+                g = mma<T>(TL::frag(s_v, t * 32 + col, f, half), gf[f], g);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = exp2_hw(fmaf(s[i], a.scale_log2, -lse2)) * (g[i] - delta);
@@ -103,44 +113,33 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
                 const u32x4 p = pack_frag<T>(s, b);
 #pragma unroll
                 for (int d = 0; d < TL::DT; ++d)
-                    dq[d] = mma<T>(TL::frag_t(s_k[buf], t * 32 + b * 2 * TL::EPC, d * 32, lane), p, dq[d]);
+                    dq[d] = mma<T>(TL::frag_t(s_k, t * 32 + b * 2 * TL::EPC, d * 32, lane), p, dq[d]);
             }
         }
-        if (more) {
-            gk.store(s_k[buf ^ 1]);
-            gv.store(s_v[buf ^ 1]);
-        }
         valid = next;
-        __syncthreads();
     }
-    if (!row_ok) return;
+    const int64_t off = pair_offset(r, j, a, a.sdq) + (row_ok ? row_offset(row, a, a.sdq) : 0);
     const int64_t slot = (static_cast<int64_t>(split) * a.n_kv * a.Hk + pair) * a.rows + row;
-    const int64_t off = pair_offset(r, j, a, a.sdq) + row_offset(row, a, a.sdq);
 #pragma unroll
-    for (int d = 0; d < TL::DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            const int at = d * 32 + 2 * i + 4 * half;
-            if (at >= a.D) continue;
-            const f32v4 x = {dq[d][i] * a.scale, dq[d][i + 1] * a.scale, dq[d][i + 2] * a.scale, dq[d][i + 3] * a.scale};
-            if constexpr (SPLIT)
-                *reinterpret_cast<f32v4 *>(a.part + slot * a.D + at) = x;
-            else
-                store4<T>(a.dq, off + at, x[0], x[1], x[2], x[3]);
-        }
+    for (int d = 0; d < TL::DT; ++d) {
+        if constexpr (SPLIT)
+            store_row_block<F32>(a.part, slot * a.D, dq[d], a.scale, d * 32, half, a.D, row_ok);
+        else
+            store_row_block<T>(a.dq, off, dq[d], a.scale, d * 32, half, a.D, row_ok);
+    }
 }
 
 // dK and dV: one workgroup owns 128 keys of one key head (a wavefront 32 of
 // them, K and V in registers) and runs over the rows of its split, queries and
 // output gradients in LDS tiles.  S and dP are formed as rows x keys, so a key
 // is a lane and P and dS are the second operands of dV^T = dO^T P and
-// dK^T = Q^T dS as they stand.
+// dK^T = Q^T dS as they stand.  A key that is not attended is a column of its
+// own, dropped at the end; its K and V are zero on the way.
 template <class T, int DP, bool SPLIT>
 __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k_attn_dkv(const AttnArgs a, int64_t block0) {
     using TL = Tile<T, DP>;
-    __shared__ __align__(16) char s_q[2][TL::kBytes];
-    __shared__ __align__(16) char s_g[2][TL::kBytes];
-    __shared__ __align__(16) float s_lse[2][TL::BN], s_delta[2][TL::BN];
+    __shared__ __align__(16) char s_qg[2][2 * TL::kBytes];  // Q tile, dO tile; two of each
+    __shared__ __align__(16) float s_stat[2][2 * TL::BN];   // lse log2(e), delta of the tile's rows
     const int tid = static_cast<int>(threadIdx.x);
     const int lane = tid & 63, wave = tid >> 6;
     const int half = lane >> 5, col = lane & 31;
@@ -175,18 +174,22 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k
     const int64_t baseq = pair_offset(r, j, a, a.sq), baseg = pair_offset(r, j, a, a.sdo);
     const float *delta = a.delta + static_cast<int64_t>(pair) * a.rows;
 
-    Staged<T, DP> gq, gg;
+    constexpr uint64_t kAll = TL::BN == 64 ? ~0ull : 0xFFFFFFFFull;
+    Loader<T, DP> gq, gg;
     float g_lse = 0.f, g_delta = 0.f;
-    const auto load = [&](int64_t row0) {
+    const auto start = [&](int64_t row0, int b) {
+        const bool all = row0 + TL::BN <= end;
+        const uint64_t valid = all ? kAll : (1ull << (end - row0)) - 1;
 #pragma unroll
         for (int i = 0; i < TL::NCH; ++i) {
-            const int id = tid + i * kAttnThreads;
-            const int64_t row = row0 + id / TL::CH;
-            const bool ok = row < end;
-            const uint32_t n = ok ? static_cast<uint32_t>(row) : 0u;
-            gq.w[i] = load_chunk<T>(a.q, baseq + row_offset(n, a, a.sq), id % TL::CH, a.D, ok);
-            gg.w[i] = load_chunk<T>(a.dout, baseg + row_offset(n, a, a.sdo), id % TL::CH, a.D, ok);
+            const int64_t row = row0 + Loader<T, DP>::row(i);
+            const uint32_t n = static_cast<uint32_t>(row < end ? row : row0);
+            const int c = Loader<T, DP>::chunk(i) * TL::EPC;
+            gq.p[i] = static_cast<const char *>(a.q) + (baseq + row_offset(n, a, a.sq) + c) * T::kSize;
+            gg.p[i] = static_cast<const char *>(a.dout) + (baseg + row_offset(n, a, a.sdo) + c) * T::kSize;
         }
+        gq.start(s_qg[b], valid, all);
+        gg.start(s_qg[b] + TL::kBytes, valid, all);
         if (tid < TL::BN) {
             const bool ok = row0 + tid < end;
             g_lse = ok ? a.lse[lse_index(r, j, static_cast<uint32_t>(row0 + tid), a)] * kLog2e : INFINITY;
@@ -194,22 +197,28 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k
         }
     };
     const auto put = [&](int b) {
-        gq.store(s_q[b]);
-        gg.store(s_g[b]);
         if (tid < TL::BN) {
-            s_lse[b][tid] = g_lse;
-            s_delta[b][tid] = g_delta;
+            s_stat[b][tid] = g_lse;
+            s_stat[b][TL::BN + tid] = g_delta;
         }
     };
     if (first < end) {
-        load(first);
-        put(0);
+        if (a.D < DP || (end - first) % TL::BN != 0) {
+            zero_lds<4 * TL::kBytes>(s_qg[0]);
+            __syncthreads();
+        }
+        gq.init(a.D);
+        gg.init(a.D);
+        start(first, 0);
     }
-    __syncthreads();
     int buf = 0;
     for (int64_t row0 = first; row0 < end; row0 += TL::BN, buf ^= 1) {
-        const bool more = row0 + TL::BN < end;
-        if (more) load(row0 + TL::BN);
+        put(buf);
+        wait_loads();
+        __syncthreads();  // the tile is here, and every wavefront has left the other one
+        const char *s_q = s_qg[buf], *s_g = s_qg[buf] + TL::kBytes;
+        const float *stat = s_stat[buf];
+        if (row0 + TL::BN < end) start(row0 + TL::BN, buf ^ 1);
 #pragma unroll
         for (int t = 0; t < TL::SUB; ++t) {
             f32x16 s, g;
@@ -217,18 +226,17 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k
             for (int i = 0; i < 16; ++i) s[i] = g[i] = 0.f;
 #pragma unroll
             for (int f = 0; f < TL::FR; ++f) {
-                s = mma<T>(TL::frag(s_q[buf], t * 32 + col, f, half), kf[f], s);
-                g = mma<T>(TL::frag(s_g[buf], t * 32 + col, f, half), vf[f], g);
+                s = mma<T>(TL::frag(s_q, t * 32 + col, f, half), kf[f], s);
+                g = mma<T>(TL::frag(s_g, t * 32 + col, f, half), vf[f], g);
             }
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
-                const f32v4 ls = *reinterpret_cast<const f32v4 *>(&s_lse[buf][t * 32 + 2 * i + 4 * half]);
-                const f32v4 de = *reinterpret_cast<const f32v4 *>(&s_delta[buf][t * 32 + 2 * i + 4 * half]);
+                const f32v4 ls = *reinterpret_cast<const f32v4 *>(stat + t * 32 + 2 * i + 4 * half);
+                const f32v4 de = *reinterpret_cast<const f32v4 *>(stat + TL::BN + t * 32 + 2 * i + 4 * half);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    const float p = key_ok ? exp2_hw(fmaf(s[i + n], a.scale_log2, -ls[n])) : 0.f;
-                    s[i + n] = p;
-                    g[i + n] = key_ok ? p * (g[i + n] - de[n]) : 0.f;
+                    s[i + n] = exp2_hw(fmaf(s[i + n], a.scale_log2, -ls[n]));
+                    g[i + n] = s[i + n] * (g[i + n] - de[n]);
                 }
             }
 #pragma unroll
@@ -236,35 +244,33 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k
                 const u32x4 p = pack_frag<T>(s, b), ds = pack_frag<T>(g, b);
 #pragma unroll
                 for (int d = 0; d < TL::DT; ++d) {
-                    dv[d] = mma<T>(TL::frag_t(s_g[buf], t * 32 + b * 2 * TL::EPC, d * 32, lane), p, dv[d]);
-                    dk[d] = mma<T>(TL::frag_t(s_q[buf], t * 32 + b * 2 * TL::EPC, d * 32, lane), ds, dk[d]);
+                    dv[d] = mma<T>(TL::frag_t(s_g, t * 32 + b * 2 * TL::EPC, d * 32, lane), p, dv[d]);
+                    dk[d] = mma<T>(TL::frag_t(s_q, t * 32 + b * 2 * TL::EPC, d * 32, lane), ds, dk[d]);
                 }
             }
         }
-        if (more) put(buf ^ 1);
-        __syncthreads();
     }
-    if (key >= a.Lk) return;
+    const bool in = key < a.Lk;
+    if (!key_ok)
+#pragma unroll
+        for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dk[d][i] = dv[d][i] = 0.f;
     const int64_t pairs = static_cast<int64_t>(a.n_kv) * a.Hk;
     const int64_t slot = (static_cast<int64_t>(split) * pairs + pair) * a.Lk + key;
     float *part_v = a.part + static_cast<int64_t>(a.n_split.d) * pairs * a.Lk * a.D;
     const int64_t offk = static_cast<int64_t>(r) * a.sdk.b + static_cast<int64_t>(j) * a.sdk.h + key * a.sdk.t;
     const int64_t offv = static_cast<int64_t>(r) * a.sdv.b + static_cast<int64_t>(j) * a.sdv.h + key * a.sdv.t;
 #pragma unroll
-    for (int d = 0; d < TL::DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            const int at = d * 32 + 2 * i + 4 * half;
-            if (at >= a.D) continue;
-            const f32v4 x = {dk[d][i] * a.scale, dk[d][i + 1] * a.scale, dk[d][i + 2] * a.scale, dk[d][i + 3] * a.scale};
-            if constexpr (SPLIT) {
-                *reinterpret_cast<f32v4 *>(a.part + slot * a.D + at) = x;
-                *reinterpret_cast<f32v4 *>(part_v + slot * a.D + at) = f32v4{dv[d][i], dv[d][i + 1], dv[d][i + 2], dv[d][i + 3]};
-            } else {
-                store4<T>(a.dk, offk + at, x[0], x[1], x[2], x[3]);
-                store4<T>(a.dv, offv + at, dv[d][i], dv[d][i + 1], dv[d][i + 2], dv[d][i + 3]);
-            }
+    for (int d = 0; d < TL::DT; ++d) {
+        if constexpr (SPLIT) {
+            store_row_block<F32>(a.part, slot * a.D, dk[d], a.scale, d * 32, half, a.D, in);
+            store_row_block<F32>(part_v, slot * a.D, dv[d], 1.f, d * 32, half, a.D, in);
+        } else {
+            store_row_block<T>(a.dk, offk, dk[d], a.scale, d * 32, half, a.D, in);
+            store_row_block<T>(a.dv, offv, dv[d], 1.f, d * 32, half, a.D, in);
         }
+    }
 }
 
 // Adds the splits' partial sums [split][pair][n][D] in split order and rounds

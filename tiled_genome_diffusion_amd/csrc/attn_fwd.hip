@@ -24,8 +24,7 @@ constexpr float kSlack = 8.f;
 template <class T, int DP, int NR, bool SPLIT>
 __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k_attn_fwd(const AttnArgs a, int64_t block0) {
     using TL = Tile<T, DP>;
-    __shared__ __align__(16) char s_k[2][TL::kBytes];
-    __shared__ __align__(16) char s_v[2][TL::kBytes];
+    __shared__ __align__(16) char s_kv[2][2 * TL::kBytes];  // K tile, V tile; two of each
     const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
     const int half = lane >> 5, col = lane & 31;
     const uint32_t bid = static_cast<uint32_t>(block0) + xcd_remap(blockIdx.x, gridDim.x);
@@ -59,26 +58,37 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
     const int64_t koff = static_cast<int64_t>(r) * a.sk.b + static_cast<int64_t>(j) * a.sk.h;
     const int64_t voff = static_cast<int64_t>(r) * a.sv.b + static_cast<int64_t>(j) * a.sv.h;
 
-    Staged<T, DP> gk, gv;
-    uint64_t valid = 0, seen = 0;
+    constexpr uint64_t kAll = TL::BN == 64 ? ~0ull : 0xFFFFFFFFull;
+    Loader<T, DP> gk, gv;
+    uint64_t valid = 0;
+    bool seen = false;
     if (first < end) {
+        if (a.D < DP || a.key_mask || (end - first) % TL::BN != 0) {
+            zero_lds<4 * TL::kBytes>(s_kv[0]);
+            __syncthreads();
+        }
+        gk.init(a.D);
+        gv.init(a.D);
+        gk.point(a.k, koff, a.sk.t, first);
+        gv.point(a.v, voff, a.sv.t, first);
         valid = valid_keys<TL::BN>(r, first, end, a);
-        gk.load_keys(a.k, koff, a.sk.t, first, valid, a.D);
-        gv.load_keys(a.v, voff, a.sv.t, first, valid, a.D);
-        gk.store(s_k[0]);
-        gv.store(s_v[0]);
+        gk.start(s_kv[0], valid, valid == kAll);
+        gv.start(s_kv[0] + TL::kBytes, valid, valid == kAll);
     }
-    __syncthreads();
+    const int64_t kstep = a.sk.t * (TL::BN * T::kSize), vstep = a.sv.t * (TL::BN * T::kSize);
     int buf = 0;
     for (int key0 = first; key0 < end; key0 += TL::BN, buf ^= 1) {
+        wait_loads();
+        __syncthreads();  // the tile is here, and every wavefront has left the other one
+        const char *s_k = s_kv[buf], *s_v = s_kv[buf] + TL::kBytes;
         uint64_t next = 0;
-        const bool more = key0 + TL::BN < end;
-        if (more) {
+        if (key0 + TL::BN < end) {
+            gk.advance(kstep);
+            gv.advance(vstep);
             next = valid_keys<TL::BN>(r, key0 + TL::BN, end, a);
-            gk.load_keys(a.k, koff, a.sk.t, key0 + TL::BN, next, a.D);
-            gv.load_keys(a.v, voff, a.sv.t, key0 + TL::BN, next, a.D);
+            gk.start(s_kv[buf ^ 1], next, next == kAll);
+            gv.start(s_kv[buf ^ 1] + TL::kBytes, next, next == kAll);
         }
-        seen |= valid;
         if (valid != 0) {
             f32x16 s[NR][TL::SUB];
 #pragma unroll
@@ -89,12 +99,12 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
                     for (int i = 0; i < 16; ++i) s[n][t][i] = 0.f;
 #pragma unroll
                 for (int f = 0; f < TL::FR; ++f) {
-                    const u32x4 kf = TL::frag(s_k[buf], t * 32 + col, f, half);
+                    const u32x4 kf = TL::frag(s_k, t * 32 + col, f, half);
 #pragma unroll
                     for (int n = 0; n < NR; ++n) s[n][t] = mma<T>(kf, qf[n][f], s[n][t]);
                 }
             }
-            if (valid != (TL::BN == 64 ? ~0ull : 0xFFFFFFFFull)) {
+            if (valid != kAll) {
 #pragma unroll
                 for (int t = 0; t < TL::SUB; ++t) {
                     const uint32_t bits = static_cast<uint32_t>(valid >> (32 * t)) >> (4 * half);
@@ -124,13 +134,16 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
                     const float m1 = fmaxf(m[n], top[n]);
                     const float fade = m1 == m[n] ? 1.f : exp2_hw((m[n] - m1) * a.scale_log2);
                     m[n] = m1;
-                    l[n] *= fade;
+                    if (seen) {  // else l and O are zero
+                        l[n] *= fade;
 #pragma unroll
-                    for (int d = 0; d < TL::DT; ++d)
+                        for (int d = 0; d < TL::DT; ++d)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[n][d][i] *= fade;
+                            for (int i = 0; i < 16; ++i) o[n][d][i] *= fade;
+                    }
                 }
             }
+            seen = true;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const float base = m[n] == -INFINITY ? 0.f : m[n] * a.scale_log2;  // all scores -inf so far: P = 0
@@ -153,25 +166,21 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
                     for (int n = 0; n < NR; ++n) p[n] = pack_frag<T>(s[n][t], b);
 #pragma unroll
                     for (int d = 0; d < TL::DT; ++d) {
-                        const u32x4 vf = TL::frag_t(s_v[buf], t * 32 + b * 2 * TL::EPC, d * 32, lane);
+                        const u32x4 vf = TL::frag_t(s_v, t * 32 + b * 2 * TL::EPC, d * 32, lane);
 #pragma unroll
                         for (int n = 0; n < NR; ++n) o[n][d] = mma<T>(vf, p[n], o[n][d]);
                     }
                 }
         }
-        if (more) {
-            gk.store(s_k[buf ^ 1]);
-            gv.store(s_v[buf ^ 1]);
-        }
         valid = next;
-        __syncthreads();
     }
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         const float total = l[n] + other_half(l[n]);
         const uint32_t row = row0 + 32 * n;
-        if (row >= a.rows) continue;
+        const bool ok = row < a.rows;
         if constexpr (SPLIT) {
+            if (!ok) continue;
             const int64_t slot = (static_cast<int64_t>(split) * a.n_kv * a.Hk + pair) * a.rows + row;
             float *part = a.part + slot * a.D;
 #pragma unroll
@@ -190,17 +199,10 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
         } else {
             // No attended key: zeros.  Attended keys whose scores are all -inf give l = 0 and NaN, as the softmax does.
             const float inv = seen ? 1.f / total : 0.f;
-            const int64_t off = pair_offset(r, j, a, a.so) + row_offset(row, a, a.so);
+            const int64_t off = pair_offset(r, j, a, a.so) + (ok ? row_offset(row, a, a.so) : 0);
 #pragma unroll
-            for (int d = 0; d < TL::DT; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const int at = d * 32 + 2 * i + 4 * half;
-                    if (at < a.D)
-                        store4<T>(a.o, off + at, o[n][d][i] * inv, o[n][d][i + 1] * inv, o[n][d][i + 2] * inv,
-                                  o[n][d][i + 3] * inv);
-                }
-            if (a.lse && half == 0) a.lse[lse_index(r, j, row, a)] = fmaf(m[n], a.scale, log2_hw(total) * kLn2);
+            for (int d = 0; d < TL::DT; ++d) store_row_block<T>(a.o, off, o[n][d], inv, d * 32, half, a.D, ok);
+            if (a.lse && half == 0 && ok) a.lse[lse_index(r, j, row, a)] = fmaf(m[n], a.scale, log2_hw(total) * kLn2);
         }
     }
 }
