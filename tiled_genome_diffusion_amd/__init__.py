@@ -9,6 +9,7 @@ libpc.so.  A negative status raises ``PCError``.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -221,6 +222,12 @@ def pc_kabsch_stitch_proper(coords, layout: PCLayout, chain, residual) -> None:
     _stitch("pc_kabsch_stitch_proper", coords, layout, chain, residual)
 
 
+# pc_attention: dtype, n_kv, group, len_q, len_k, heads, heads_kv, dim, scale, then (batch, token, head) strides of
+# q, k, v, out, dout, dq, dk, dv.  pc_norm_side: batch, len, heads, x, y, weight, positions, their stride, dy, dx,
+# dweight, then the strides of x, y, dy, dx.  Packed by struct: a tenth of a ctypes structure's time, and small calls are
+# bound by the host.
+_ATTENTION = struct.Struct("@8if24q")
+_NORM_SIDE = struct.Struct("@3i4Pq3P12q")
 _DTYPES: dict = {}
 
 
@@ -232,82 +239,100 @@ def _dtype(t, name: str) -> int:
     d = _DTYPES.get(t.dtype)
     if d is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
     return d
 
 
 def _like(t, name: str, shape, ref):
-    """Device pointer of a [batch, len, heads, dim] tensor on ref's device and of its type; heads are contiguous."""
-    if not t.is_cuda or t.device != ref.device:
-        raise ValueError(f"{name} must be a device tensor on {ref.device}")
-    if t.dtype != ref.dtype:
-        raise ValueError(f"{name} must be {ref.dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(3) != 1:
-        raise ValueError(f"{name}: the values of a head must be contiguous")
-    return t.data_ptr()
+    """(address, strides) of a [batch, len, heads, dim] tensor on ref's device and of its type, heads contiguous."""
+    stride = t.stride()
+    if t.device != ref.device or t.dtype != ref.dtype or t.shape != shape or stride[3] != 1:
+        raise ValueError(f"{name} must be {ref.dtype} of shape {tuple(shape)} on {ref.device} with the values of a head "
+                         f"contiguous, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {stride}")
+    return t.data_ptr(), stride
 
 
 def _heads_of(t, name: str):
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [batch, len, heads, dim], got {tuple(t.shape)}")
-    return t.shape
+    s = t.shape
+    if len(s) != 4:
+        raise ValueError(f"{name} must be [batch, len, heads, dim], got {tuple(s)}")
+    return s
 
 
 def _flat(t, name: str, dtype, shape, ref):
-    """Device pointer of a contiguous tensor of the given type and shape on ref's device, or None."""
+    """Address of a contiguous tensor of the given type and shape on ref's device, or None."""
     if t is None:
         return None
-    if not t.is_cuda or t.device != ref.device:
-        raise ValueError(f"{name} must be a device tensor on {ref.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != ref.device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)} on {ref.device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _enqueue(ref, func, *args):
     """func(*args, stream) on ref's device and torch's current stream there."""
-    cuda = _torch().cuda
-    if cuda.current_device() == ref.device.index:
-        return func(*args, cuda.current_stream().cuda_stream)
-    with cuda.device(ref.device):
-        return func(*args, cuda.current_stream().cuda_stream)
+    m = _torch()
+    at = ref.device.index
+    if m.cuda.current_device() == at:
+        return func(*args, m._C._cuda_getCurrentRawStream(at))
+    with m.cuda.device(ref.device):
+        return func(*args, m._C._cuda_getCurrentRawStream(at))
 
 
-def _workspace(given, need: int, ref):
-    """(pointer, bytes, owner) of a workspace: the caller's, or one from torch's allocator on the current stream."""
+def _workspace(given, need, ref):
+    """(address, bytes, owner) of a workspace: the caller's, or one from torch's allocator on the current stream.
+    need() gives the bytes."""
     if given is None:
-        if need == 0:
+        n = need()
+        if n == 0:
             return None, 0, None
-        given = _torch().empty(need, dtype=_torch().uint8, device=ref.device)
-    elif not given.is_cuda or given.device != ref.device or not given.is_contiguous():
+        given = _torch().empty(n, dtype=_torch().uint8, device=ref.device)
+    elif given.device != ref.device or not given.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {ref.device}")
     return given.data_ptr(), given.numel() * given.element_size(), given
 
 
-def _attention(q, k, v, scale):
+def _attention_sizes(q, k, scale):
+    """(dtype .. scale) of pc_attention."""
     (B, Lq, H, D), (R, Lk, Hk, Dk) = _heads_of(q, "q"), _heads_of(k, "k")
     if Dk != D:
         raise ValueError(f"q has heads of {D} values, k of {Dk}")
     if (B % R != 0) if R else B:
         raise ValueError(f"{R} encoder states must divide {B} query batches")
-    a = _lib.Attention(_dtype(q, "q"), R, B // R if R else 0, Lq, Lk, H, Hk, D, D ** -0.5 if scale is None else scale)
-    a.q, a.k, a.v = q.stride()[:3], k.stride()[:3], v.stride()[:3]
-    return a
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    return _dtype(q, "q"), R, B // R if R else 0, Lq, Lk, H, Hk, D, scale
+
+
+def _mask(m):
+    """A key mask as bytes."""
+    t = _torch()
+    return m.view(t.uint8) if m is not None and m.dtype == t.bool else m
+
+
+_NO_STRIDES = (0,) * 15
+
+
+def _attention_bytes(a: bytes, backward: bool, func: str) -> int:
+    n = ctypes.c_int64()
+    _check(_lib.load().pc_cross_attention_workspace(a, int(backward), ctypes.addressof(n)), func)
+    return n.value
 
 
 def pc_cross_attention_workspace(q, k, v, backward: bool = False, scale=None) -> int:
     """Bytes of workspace of pc_cross_attention (or its backward) for these tensors."""
-    a = _attention(q, k, v, scale)
-    a.out = q.stride()[:3]
-    if backward:
-        a.dout, a.dq, a.dk, a.dv = a.q, a.q, a.k, a.v
-    n = ctypes.c_int64()
-    _check(_lib.load().pc_cross_attention_workspace(ctypes.addressof(a), int(backward), ctypes.addressof(n)),
-           "pc_cross_attention_workspace")
-    return n.value
+    (_, sq), (_, sk), (_, sv) = _like(q, "q", _heads_of(q, "q"), q), _like(k, "k", _heads_of(k, "k"), q), _like(v, "v", k.shape, q)
+    q3, k3 = sq[:3], sk[:3]
+    a = _ATTENTION.pack(*_attention_sizes(q, k, scale), *q3, *k3, *sv[:3], *_dense(q.shape),
+                        *(_dense(q.shape) * 2 + _dense(k.shape) * 2 if backward else _NO_STRIDES[:12]))
+    return _attention_bytes(a, backward, "pc_cross_attention_workspace")
+
+
+def _dense(shape):
+    """Strides of a contiguous [batch, len, heads, dim] tensor."""
+    _, L, H, D = shape
+    return L * H * D, H * D, D
 
 
 def pc_cross_attention(q, k, v, out, lse=None, kv_len=None, key_mask=None, scale=None, workspace=None) -> None:
@@ -316,61 +341,67 @@ def pc_cross_attention(q, k, v, out, lse=None, kv_len=None, key_mask=None, scale
     lse float32 [n_kv * group, len_q, heads]; kv_len int32 [n_kv]; key_mask uint8 or bool [n_kv, len_k]; scale defaults
     to dim ** -0.5.  Without a workspace one is taken from torch's allocator where it is needed."""
     t = _torch()
-    lib = _lib.load()
-    a = _attention(q, k, v, scale)
-    R, Lk = k.shape[0], k.shape[1]
-    ptrs = (_like(q, "q", q.shape, q), _like(k, "k", k.shape, q), _like(v, "v", k.shape, q),
-            _flat(kv_len, "kv_len", t.int32, (R,), q),
-            _flat(key_mask.view(t.uint8) if key_mask is not None and key_mask.dtype == t.bool else key_mask, "key_mask",
-                  t.uint8, (R, Lk), q),
-            _like(out, "out", q.shape, q), _flat(lse, "lse", t.float32, q.shape[:3], q))
-    a.out = out.stride()[:3]
-    n = ctypes.c_int64()
-    _check(lib.pc_cross_attention_workspace(ctypes.addressof(a), 0, ctypes.addressof(n)), "pc_cross_attention")
-    p, size, keep = _workspace(workspace, n.value, q)
-    _check(_enqueue(q, lib.pc_cross_attention, ctypes.addressof(a), *ptrs, p, size), "pc_cross_attention")
+    sizes = _attention_sizes(q, k, scale)
+    shape, kshape = q.shape, k.shape
+    (pq, sq), (pk, sk), (pv, sv) = _like(q, "q", shape, q), _like(k, "k", kshape, q), _like(v, "v", kshape, q)
+    po, so = _like(out, "out", shape, q)
+    a = _ATTENTION.pack(*sizes, *sq[:3], *sk[:3], *sv[:3], *so[:3], *_NO_STRIDES[:12])
+    ptrs = (pq, pk, pv, _flat(kv_len, "kv_len", t.int32, kshape[:1], q),
+            _flat(_mask(key_mask), "key_mask", t.uint8, kshape[:2], q), po,
+            _flat(lse, "lse", t.float32, shape[:3], q))
+    p, size, keep = _workspace(workspace, lambda: _attention_bytes(a, False, "pc_cross_attention"), q)
+    _check(_enqueue(q, _lib.load().pc_cross_attention, a, *ptrs, p, size), "pc_cross_attention")
 
 
 def pc_cross_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, kv_len=None, key_mask=None, scale=None,
                                 workspace=None) -> None:
     """dq, dk, dv of pc_cross_attention from its inputs, out, lse and dout (arguments as there)."""
     t = _torch()
-    lib = _lib.load()
-    a = _attention(q, k, v, scale)
-    R, Lk = k.shape[0], k.shape[1]
+    sizes = _attention_sizes(q, k, scale)
+    shape, kshape = q.shape, k.shape
     if lse is None:
         raise ValueError("lse of the forward call is required")
-    first = (_like(q, "q", q.shape, q), _like(k, "k", k.shape, q), _like(v, "v", k.shape, q),
-             _like(out, "out", q.shape, q), _flat(lse, "lse", t.float32, q.shape[:3], q),
-             _like(dout, "dout", q.shape, q), _flat(kv_len, "kv_len", t.int32, (R,), q),
-             _flat(key_mask.view(t.uint8) if key_mask is not None and key_mask.dtype == t.bool else key_mask,
-                   "key_mask", t.uint8, (R, Lk), q),
-             _like(dq, "dq", q.shape, q), _like(dk, "dk", k.shape, q), _like(dv, "dv", k.shape, q))
-    a.out, a.dout = out.stride()[:3], dout.stride()[:3]
-    a.dq, a.dk, a.dv = dq.stride()[:3], dk.stride()[:3], dv.stride()[:3]
-    n = ctypes.c_int64()
-    _check(lib.pc_cross_attention_workspace(ctypes.addressof(a), 1, ctypes.addressof(n)),
-           "pc_cross_attention_backward")
-    p, size, keep = _workspace(workspace, n.value, q)
-    _check(_enqueue(q, lib.pc_cross_attention_backward, ctypes.addressof(a), *first, p, size),
-           "pc_cross_attention_backward")
+    (pq, sq), (pk, sk), (pv, sv) = _like(q, "q", shape, q), _like(k, "k", kshape, q), _like(v, "v", kshape, q)
+    (po, so), (pg, sg) = _like(out, "out", shape, q), _like(dout, "dout", shape, q)
+    (pdq, sdq), (pdk, sdk), (pdv, sdv) = _like(dq, "dq", shape, q), _like(dk, "dk", kshape, q), _like(dv, "dv", kshape, q)
+    a = _ATTENTION.pack(*sizes, *sq[:3], *sk[:3], *sv[:3], *so[:3], *sg[:3], *sdq[:3], *sdk[:3], *sdv[:3])
+    ptrs = (pq, pk, pv, po, _flat(lse, "lse", t.float32, shape[:3], q), pg,
+            _flat(kv_len, "kv_len", t.int32, kshape[:1], q),
+            _flat(_mask(key_mask), "key_mask", t.uint8, kshape[:2], q), pdq, pdk, pdv)
+    p, size, keep = _workspace(workspace, lambda: _attention_bytes(a, True, "pc_cross_attention_backward"), q)
+    _check(_enqueue(q, _lib.load().pc_cross_attention_backward, a, *ptrs, p, size), "pc_cross_attention_backward")
 
 
-def _norm_side(x, weight, positions, ref, name: str):
-    t = _torch()
-    B, L, H, D = _heads_of(x, name)
-    s = _lib.NormSide(B, L, H, _like(x, name, x.shape, ref))
-    s.weight = _flat(weight, name + "_weight", t.float32, (D,), ref)
-    s.sx = x.stride()[:3]
-    if positions is not None:
-        if not positions.is_cuda or positions.device != ref.device or positions.dtype != t.int32:
-            raise ValueError(f"{name}_positions must be int32 on {ref.device}")
-        if tuple(positions.shape) not in ((L,), (1, L), (B, L)) or (L > 1 and positions.stride(-1) != 1):
-            raise ValueError(f"{name}_positions must be [{L}] or [{B}, {L}] with contiguous rows, "
-                             f"got {tuple(positions.shape)}")
-        s.positions = positions.data_ptr()
-        s.positions_stride = positions.stride(0) if positions.dim() == 2 and positions.shape[0] > 1 else 0
-    return s
+def _positions(p, B: int, L: int, ref, name: str):
+    """(address, stride between batches) of int32 positions [L], [1, L] or [B, L]."""
+    if p is None:
+        return None, 0
+    s = p.shape
+    if p.device != ref.device or p.dtype != _torch().int32 or not (s == (B, L) or s == (L,) or s == (1, L)) or \
+            (L > 1 and p.stride(-1) != 1):
+        raise ValueError(f"{name}_positions must be int32 [{L}] or [{B}, {L}] with contiguous rows on {ref.device}, "
+                         f"got {p.dtype} {tuple(s)} on {p.device}")
+    return p.data_ptr(), p.stride(0) if len(s) == 2 and s[0] > 1 else 0
+
+
+def _norm_side(name: str, ref, x, weight=None, positions=None, y=None, dy=None, dx=None, dweight=None, strides=None):
+    """pc_norm_side of one side, packed; None for a side that is left out."""
+    if x is None:
+        return None
+    shape = _heads_of(x, name)
+    B, L, H, D = shape
+    f32 = _torch().float32
+    px, sx = _like(x, name, shape, ref)
+    py = pdy = pdx = None
+    sy = sdy = sdx = strides or _NO_STRIDES
+    if y is not None:
+        py, sy = _like(y, name + "_out", shape, ref)
+    if dy is not None:
+        (pdy, sdy), (pdx, sdx) = _like(dy, f"d{name}_out", shape, ref), _like(dx, "d" + name, shape, ref)
+    pos, pos_b = _positions(positions, B, L, ref, name)
+    return _NORM_SIDE.pack(B, L, H, px, py or 0, _flat(weight, name + "_weight", f32, shape[3:], ref) or 0, pos or 0, pos_b,
+                           pdy or 0, pdx or 0, _flat(dweight, f"d{name}_weight", f32, shape[3:], ref) or 0,
+                           *sx[:3], *sy[:3], *sdy[:3], *sdx[:3])
 
 
 def _freqs(freqs):
@@ -382,8 +413,7 @@ def _norm_ref(q, k):
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q and k are both None")
-    _heads_of(ref, "q" if q is not None else "k")
-    if q is not None and k is not None and _heads_of(k, "k")[3] != q.shape[3]:
+    if q is not None and k is not None and _heads_of(k, "k")[3] != _heads_of(q, "q")[3]:
         raise ValueError(f"q has heads of {q.shape[3]} values, k of {k.shape[3]}")
     return ref
 
@@ -395,64 +425,42 @@ def pc_qk_norm_rope(q, k, q_weight, k_weight, q_positions, k_positions, freqs, q
 
     Weights float32 [dim] or None; positions int32 [batch, len] or [len], or None for 0 .. len - 1; freqs radians per
     position of each pair (float64, host).  q or k may be None, with its other arguments."""
-    lib = _lib.load()
     ref = _norm_ref(q, k)
-    sides = []
-    for x, w, pos, out, name in ((q, q_weight, q_positions, q_out, "q"), (k, k_weight, k_positions, k_out, "k")):
-        s = None
-        if x is not None:
-            s = _norm_side(x, w, pos, ref, name)
-            s.y, s.sy = _like(out, name + "_out", x.shape, ref), out.stride()[:3]
-        sides.append(s)
+    dtype = _dtype(ref, "q" if q is not None else "k")
+    sq = _norm_side("q", ref, q, q_weight, q_positions, q_out)
+    sk = _norm_side("k", ref, k, k_weight, k_positions, k_out)
     f, fp = _freqs(freqs)
-    p = [None if s is None else ctypes.addressof(s) for s in sides]
-    _check(_enqueue(ref, lib.pc_qk_norm_rope, *p, _dtype(ref, "q"), ref.shape[3], 2 * f.size, fp, int(bool(interleaved)),
-                    float(eps)), "pc_qk_norm_rope")
+    _check(_enqueue(ref, _lib.load().pc_qk_norm_rope, sq, sk, dtype, ref.shape[3], 2 * f.size, fp,
+                    1 if interleaved else 0, eps), "pc_qk_norm_rope")
+
+
+def _norm_bytes(sq, sk, dtype: int, dim: int, rot: int, func: str) -> int:
+    n = ctypes.c_int64()
+    _check(_lib.load().pc_qk_norm_rope_workspace(sq, sk, dtype, dim, rot, ctypes.addressof(n)), func)
+    return n.value
 
 
 def pc_qk_norm_rope_workspace(q, k, freqs) -> int:
     """Bytes of workspace of pc_qk_norm_rope_backward for these tensors."""
     ref = _norm_ref(q, k)
-    sides = []
-    for x, name in ((q, "q"), (k, "k")):
-        s = None
-        if x is not None:
-            s = _norm_side(x, None, None, ref, name)
-            s.sdy = s.sdx = s.sx
-        sides.append(s)
-    n = ctypes.c_int64()
-    p = [None if s is None else ctypes.addressof(s) for s in sides]
-    _check(_lib.load().pc_qk_norm_rope_workspace(*p, _dtype(ref, "q"), ref.shape[3], 2 * len(freqs),
-                                                 ctypes.addressof(n)), "pc_qk_norm_rope_workspace")
-    return n.value
+    dtype = _dtype(ref, "q" if q is not None else "k")
+    sides = [_norm_side(n, ref, x, strides=None if x is None else _dense(_heads_of(x, n))) for n, x in (("q", q), ("k", k))]
+    return _norm_bytes(*sides, dtype, ref.shape[3], 2 * len(freqs), "pc_qk_norm_rope_workspace")
 
 
 def pc_qk_norm_rope_backward(q, k, q_weight, k_weight, q_positions, k_positions, freqs, dq_out, dk_out, dq, dk,
                              dq_weight=None, dk_weight=None, eps: float = 1e-6, interleaved: bool = False,
                              workspace=None) -> None:
     """Gradients of pc_qk_norm_rope: dq, dk (which may be dq_out, dk_out) and, where given, dq_weight and dk_weight."""
-    t = _torch()
-    lib = _lib.load()
     ref = _norm_ref(q, k)
-    sides = []
-    for x, w, pos, dy, dx, dw, name in ((q, q_weight, q_positions, dq_out, dq, dq_weight, "q"),
-                                        (k, k_weight, k_positions, dk_out, dk, dk_weight, "k")):
-        s = None
-        if x is not None:
-            s = _norm_side(x, w, pos, ref, name)
-            s.dy, s.sdy = _like(dy, f"d{name}_out", x.shape, ref), dy.stride()[:3]
-            s.dx, s.sdx = _like(dx, f"d{name}", x.shape, ref), dx.stride()[:3]
-            s.dweight = _flat(dw, f"d{name}_weight", t.float32, (x.shape[3],), ref)
-        sides.append(s)
+    dtype = _dtype(ref, "q" if q is not None else "k")
+    sq = _norm_side("q", ref, q, q_weight, q_positions, None, dq_out, dq, dq_weight)
+    sk = _norm_side("k", ref, k, k_weight, k_positions, None, dk_out, dk, dk_weight)
     f, fp = _freqs(freqs)
-    p = [None if s is None else ctypes.addressof(s) for s in sides]
     D = ref.shape[3]
-    n = ctypes.c_int64()
-    _check(lib.pc_qk_norm_rope_workspace(*p, _dtype(ref, "q"), D, 2 * f.size, ctypes.addressof(n)),
-           "pc_qk_norm_rope_backward")
-    wp, size, keep = _workspace(workspace, n.value, ref)
-    _check(_enqueue(ref, lib.pc_qk_norm_rope_backward, *p, _dtype(ref, "q"), D, 2 * f.size, fp, int(bool(interleaved)),
-                    float(eps), wp, size), "pc_qk_norm_rope_backward")
+    p, size, keep = _workspace(workspace, lambda: _norm_bytes(sq, sk, dtype, D, 2 * f.size, "pc_qk_norm_rope_backward"), ref)
+    _check(_enqueue(ref, _lib.load().pc_qk_norm_rope_backward, sq, sk, dtype, D, 2 * f.size, fp, 1 if interleaved else 0,
+                    eps, p, size), "pc_qk_norm_rope_backward")
 
 
 def pc_set_max_dispatch_items(items: int) -> None:

@@ -21,25 +21,6 @@ class Layout(ctypes.Structure):
                 ("chain_len", ctypes.c_int32), ("overlap", ctypes.c_int32)]
 
 
-class Strides(ctypes.Structure):
-    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
-
-
-class Attention(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("group", ctypes.c_int32),
-                ("len_q", ctypes.c_int32), ("len_k", ctypes.c_int32), ("heads", ctypes.c_int32),
-                ("heads_kv", ctypes.c_int32), ("dim", ctypes.c_int32), ("scale", ctypes.c_float),
-                ("q", Strides), ("k", Strides), ("v", Strides), ("out", Strides),
-                ("dout", Strides), ("dq", Strides), ("dk", Strides), ("dv", Strides)]
-
-
-class NormSide(ctypes.Structure):
-    _fields_ = [("batch", ctypes.c_int32), ("len", ctypes.c_int32), ("heads", ctypes.c_int32),
-                ("x", vp), ("y", vp), ("weight", vp), ("positions", vp), ("positions_stride", ctypes.c_int64),
-                ("dy", vp), ("dx", vp), ("dweight", vp),
-                ("sx", Strides), ("sy", Strides), ("sdy", Strides), ("sdx", Strides)]
-
-
 # name -> (restype, argtypes), in the order of include/pc.h
 SIGNATURES = {
     "pc_version": (ctypes.c_char_p, []),

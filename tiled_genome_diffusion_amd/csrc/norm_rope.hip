@@ -106,7 +106,11 @@ __device__ __forceinline__ int64_t head_offset(uint32_t token, uint32_t h, const
 }
 
 // Forward and, with BWD, the gradients.  A workgroup takes tiles of `tile`
-// tokens, all heads of each; queries' workgroups come first in the grid.
+// tokens, all heads of each; queries' workgroups come first in the grid.  The
+// rows of a tile are taken kUnroll per lane at a time, all loads ahead of the
+// arithmetic (and the first ones ahead of the tile's table).
+constexpr int kUnroll = 4;
+
 template <class T, int LPR, bool INTER, bool BWD>
 __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, int64_t block0) {
     using RL = RowLanes<T, LPR>;
@@ -133,59 +137,74 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, in
     for (uint32_t tile = blk; tile < s.tiles; tile += s.blocks) {
         const int64_t token0 = static_cast<int64_t>(tile) * a.tile;
         const int n_tokens = static_cast<int>(s.tokens - token0 < a.tile ? s.tokens - token0 : a.tile);
-        if (BWD) __syncthreads();  // the previous tile's table has been read
-        fill_table(a, s, token0, n_tokens, s_cs);
-        __syncthreads();
         const int n_rows = n_tokens * static_cast<int>(s.heads.d);
-        for (int row0 = 0; row0 < n_rows; row0 += RL::kRows) {
-            const int row = row0 + tid / LPR;
-            const bool ok = live && row < n_rows;
-            const uint32_t t = div_by(static_cast<uint32_t>(row), s.heads), h = row - t * s.heads.d;
-            const uint32_t token = static_cast<uint32_t>(token0) + t;
-            const float2 *cs = s_cs + t * a.half;
-            u32x4 raw = {0u, 0u, 0u, 0u}, graw = {0u, 0u, 0u, 0u};
-            if (ok) {
-                raw = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(s.x) +
-                                                       (head_offset(token, h, s, s.sx) + e0) * T::kSize);
-                if (BWD)
-                    graw = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(s.dy) +
-                                                            (head_offset(token, h, s, s.sdy) + e0) * T::kSize);
+        for (int row0 = 0; row0 < n_rows; row0 += kUnroll * RL::kRows) {
+            u32x4 raw[kUnroll], graw[kUnroll];
+            int at[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int row = row0 + u * RL::kRows + tid / LPR;
+                const bool ok = live && row < n_rows;
+                const uint32_t t = div_by(static_cast<uint32_t>(row), s.heads), h = row - t * s.heads.d;
+                at[u] = ok ? static_cast<int>(t) : -1;
+                raw[u] = graw[u] = u32x4{0u, 0u, 0u, 0u};
+                if (ok) {
+                    const uint32_t token = static_cast<uint32_t>(token0) + t;
+                    raw[u] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(s.x) +
+                                                              (head_offset(token, h, s, s.sx) + e0) * T::kSize);
+                    if (BWD)
+                        graw[u] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(s.dy) +
+                                                                   (head_offset(token, h, s, s.sdy) + e0) * T::kSize);
+                }
             }
-            float x[EPC];
-            unpack_chunk<T>(raw, x);
-            float q = 0.f;
+            if (row0 == 0) {
+                __syncthreads();  // the previous tile's table has been read
+                fill_table(a, s, token0, n_tokens, s_cs);
+                __syncthreads();
+            }
 #pragma unroll
-            for (int i = 0; i < EPC; ++i) q = fmaf(x[i], x[i], q);
-            const float rstd = 1.f / sqrtf(fmaf(RL::sum(q), a.inv_d, a.eps));
-            if constexpr (!BWD) {
-                float n[EPC], pn[EPC], y[EPC];
-                if constexpr (!INTER) unpack_chunk<T>(partner_chunk<LPR>(raw, src), pn);
+            for (int u = 0; u < kUnroll; ++u) {
+                const bool ok = at[u] >= 0;
+                const uint32_t row = static_cast<uint32_t>(row0 + u * RL::kRows + tid / LPR);
+                const uint32_t t = ok ? at[u] : 0, h = row - t * s.heads.d;
+                const uint32_t token = static_cast<uint32_t>(token0) + t;
+                const float2 *cs = s_cs + t * a.half;
+                float x[EPC];
+                unpack_chunk<T>(raw[u], x);
+                float q = 0.f;
 #pragma unroll
-                for (int i = 0; i < EPC; ++i) {
-                    y[i] = n[i] = x[i] * rstd * w[i];
-                    if constexpr (!INTER) pn[i] = pn[i] * rstd * pw[i];
+                for (int i = 0; i < EPC; ++i) q = fmaf(x[i], x[i], q);
+                const float rstd = 1.f / sqrtf(fmaf(RL::sum(q), a.inv_d, a.eps));
+                if constexpr (!BWD) {
+                    float n[EPC], pn[EPC], y[EPC];
+                    if constexpr (!INTER) unpack_chunk<T>(partner_chunk<LPR>(raw[u], src), pn);
+#pragma unroll
+                    for (int i = 0; i < EPC; ++i) {
+                        y[i] = n[i] = x[i] * rstd * w[i];
+                        if constexpr (!INTER) pn[i] = pn[i] * rstd * pw[i];
+                    }
+                    if (turned && ok) rotate<EPC, INTER>(n, pn, cs, e0, a.half, 1.f, y);
+                    if (ok) store_chunk<T>(s.y, head_offset(token, h, s, s.sy) + e0, y);
+                } else {
+                    float g[EPC], pg[EPC], v[EPC];
+                    unpack_chunk<T>(graw[u], g);
+                    if constexpr (!INTER) unpack_chunk<T>(partner_chunk<LPR>(graw[u], src), pg);
+#pragma unroll
+                    for (int i = 0; i < EPC; ++i) v[i] = g[i];
+                    if (turned && ok) rotate<EPC, INTER>(g, pg, cs, e0, a.half, -1.f, v);
+                    float dot = 0.f;
+#pragma unroll
+                    for (int i = 0; i < EPC; ++i) {
+                        x[i] *= rstd;
+                        if (ok) dw[i] = fmaf(v[i], x[i], dw[i]);
+                        v[i] *= w[i];
+                        dot = fmaf(v[i], x[i], dot);
+                    }
+                    const float mean = RL::sum(dot) * a.inv_d;
+#pragma unroll
+                    for (int i = 0; i < EPC; ++i) v[i] = rstd * fmaf(-mean, x[i], v[i]);
+                    if (ok) store_chunk<T>(s.dx, head_offset(token, h, s, s.sdx) + e0, v);
                 }
-                if (turned && ok) rotate<EPC, INTER>(n, pn, cs, e0, a.half, 1.f, y);
-                if (ok) store_chunk<T>(s.y, head_offset(token, h, s, s.sy) + e0, y);
-            } else {
-                float g[EPC], pg[EPC], u[EPC];
-                unpack_chunk<T>(graw, g);
-                if constexpr (!INTER) unpack_chunk<T>(partner_chunk<LPR>(graw, src), pg);
-#pragma unroll
-                for (int i = 0; i < EPC; ++i) u[i] = g[i];
-                if (turned && ok) rotate<EPC, INTER>(g, pg, cs, e0, a.half, -1.f, u);
-                float dot = 0.f;
-#pragma unroll
-                for (int i = 0; i < EPC; ++i) {
-                    x[i] *= rstd;
-                    dw[i] = fmaf(u[i], x[i], dw[i]);
-                    u[i] *= w[i];
-                    dot = fmaf(u[i], x[i], dot);
-                }
-                const float mean = RL::sum(dot) * a.inv_d;
-#pragma unroll
-                for (int i = 0; i < EPC; ++i) u[i] = rstd * fmaf(-mean, x[i], u[i]);
-                if (ok) store_chunk<T>(s.dx, head_offset(token, h, s, s.sdx) + e0, u);
             }
         }
     }
@@ -193,7 +212,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, in
         if (!s.dw) return;
         // Sum of the workgroup's row groups, in their order.
         __syncthreads();
-        float *sum = reinterpret_cast<float *>(s_cs);  // [kRows][LPR * EPC] at most 8 KB
+        float *sum = reinterpret_cast<float *>(s_cs);  // [kRows][LPR * EPC]: 8 KB at most
 #pragma unroll
         for (int i = 0; i < EPC; ++i) sum[(tid / LPR) * (LPR * EPC) + e0 + i] = dw[i];
         __syncthreads();
@@ -205,31 +224,39 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, in
     }
 }
 
-// dw = sum of the workgroups' partial sums: lane (d, g) adds every 8th of them
-// in order, then the eight are added in order.  Workgroup 0: queries, 1: keys.
+// dw = sum of the workgroups' partial sums, a workgroup per side and 32
+// values: lane (g, d) adds every 32nd of them in order, then the 32 sums are
+// added in order.
 __global__ __launch_bounds__(1024) void k_norm_dw(const NormArgs a, int64_t block0) {
-    __shared__ float s_sum[8][128];
-    const NormSide &s = a.side[block0 + blockIdx.x];
+    __shared__ float s_sum[32][33];
+    const int id = static_cast<int>(block0 + blockIdx.x), n = (a.D + 31) / 32;
+    const NormSide &s = a.side[id / n];
     if (!s.dw) return;
-    const int d = static_cast<int>(threadIdx.x) & 127, g = static_cast<int>(threadIdx.x) >> 7;
+    const int l = static_cast<int>(threadIdx.x) & 31, g = static_cast<int>(threadIdx.x) >> 5;
+    const int d = (id % n) * 32 + l;
     float v = 0.f;
     if (d < a.D)
-        for (uint32_t b = g; b < s.blocks; b += 8) v += s.part[static_cast<int64_t>(b) * a.D + d];
-    s_sum[g][d] = v;
+#pragma unroll 4
+        for (uint32_t b = g; b < s.blocks; b += 32) v += s.part[static_cast<int64_t>(b) * a.D + d];
+    s_sum[g][l] = v;
     __syncthreads();
     if (g == 0 && d < a.D) {
-        for (int i = 1; i < 8; ++i) v += s_sum[i][d];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) v += s_sum[i][l];
         s.dw[d] = v;
     }
 }
 
 constexpr uint32_t kBwdBlocks = 1024;  // of a side: its tiles are dealt to at most this many workgroups
 
-// Tokens per tile: about 8 KB of rows, as many as the table holds.
+// Tokens per tile: the rows a workgroup holds in kUnroll steps (of the side
+// that has more tokens), as many as the table holds.
 void plan(NormArgs &a, int32_t dtype, bool bwd) {
-    const uint32_t size = dtype == kF32 ? 4 : 2;
-    const uint32_t heads = a.side[0].tokens ? a.side[0].heads.d : a.side[1].heads.d;
-    uint32_t tile = 16384u / (static_cast<uint32_t>(a.D) * size * heads);
+    const uint32_t chunks = static_cast<uint32_t>(a.D) * (dtype == kF32 ? 4 : 2) / 16;
+    uint32_t lanes = 4;
+    while (lanes < chunks) lanes *= 2;
+    const uint32_t heads = a.side[a.side[1].tokens > a.side[0].tokens ? 1 : 0].heads.d;
+    uint32_t tile = kUnroll * (kNormThreads / lanes) / heads;
     const uint32_t most = a.half > 0 ? kTableBytes / (8u * a.half) : 64u;
     tile = tile < 1 ? 1 : tile;
     a.tile = tile > most ? most : tile;
@@ -286,7 +313,7 @@ hipError_t launch_norm_bwd(NormArgs &a, int32_t dtype, bool interleaved, char *w
     a.side[1].part = a.side[0].part + static_cast<int64_t>(a.side[0].blocks) * a.D;
     const hipError_t e = launch<true>(a, dtype, interleaved, stream);
     if (e != hipSuccess || (!a.side[0].dw && !a.side[1].dw)) return e;
-    return launch_slices(2, 1024, [&](int64_t first, uint32_t count) {
+    return launch_slices(2 * ((a.D + 31) / 32), 1024, [&](int64_t first, uint32_t count) {
         k_norm_dw<<<count, 1024, 0, stream>>>(a, first);
     });
 }
