@@ -11,7 +11,7 @@
 // Angles.  Each frequency arrives as turns per position in 64-bit fixed point,
 // so position times frequency modulo one turn is an integer product's low 64
 // bits: exact to 2^-64 turns per position for any 32-bit position, where a
-// float32 product would lose all digits of the angle at large positions.  The
+// float32 product would lose the angle's digits at large positions.  The
 // top 32 bits as a float in [-1/2, 1/2) go to v_sin / v_cos, which take turns
 // (error <= 1.3e-7 of each, common.hpp).
 #include "launch.hpp"
@@ -21,8 +21,8 @@ namespace pc {
 namespace {
 
 constexpr int kNormThreads = 256;
-// cos and sin of a workgroup's tokens in LDS.
-constexpr int kTableBytes = 16384;
+// Factors of a workgroup's tokens in LDS.
+constexpr int kTableBytes = 32768;
 
 // A head's row is held by LPR lanes of 16 bytes each, the lane's chunk the
 // same for every row it visits, so its weights stay in registers.
@@ -31,59 +31,63 @@ struct RowLanes {
     static constexpr int EPC = 16 / T::kSize;
     static constexpr int kRows = kNormThreads / LPR;  // rows a workgroup holds at once
 
-    // Sum over the LPR lanes of a row (the same bits in each).
+    // Sum over the LPR lanes of a row (the same bits in each): quad permutes,
+    // then the half-row and row mirrors, as wave_sum.
     __device__ static __forceinline__ float sum(float v) {
-#pragma unroll
-        for (int m = 1; m < LPR; m <<= 1) v += __shfl_xor(v, m, 64);
+        v += dpp<0xB1>(v);
+        v += dpp<0x4E>(v);
+        if constexpr (LPR > 4) v += dpp<0x141>(v);
+        if constexpr (LPR > 8) v += dpp<0x140>(v);
+        if constexpr (LPR > 16) v += __shfl_xor(v, 16, 64);
         return v;
     }
 };
 
-// cos, sin of the tile's tokens: s_cs[token][pair].
+// The rotation as two factors per value: with value e's partner p(e),
+//   y[e] = c[e] n[e] + s[e] n[p(e)];
+// c = cos and s = -sin (first of a pair) or sin (second), and c = 1, s = 0 past
+// the rotated values.  s_tab[token] holds c of the D values, then s: with the
+// weights multiplied in (forward: n = x rstd w), or for the inverse rotation,
+// s negated, without them (backward).  The factors are formed once per token
+// and serve all its heads.
+template <bool INTER, bool BWD>
 __device__ __forceinline__ void fill_table(const NormArgs &a, const NormSide &s, int64_t token0, int n_tokens,
-                                           float2 *s_cs) {
-    for (int id = static_cast<int>(threadIdx.x); id < n_tokens * a.half; id += kNormThreads) {
-        const int t = id / a.half, i = id - t * a.half;
-        const uint32_t token = static_cast<uint32_t>(token0 + t);
-        const uint32_t b = div_by(token, s.len), at = token - b * s.len.d;
-        const int64_t p = s.pos ? s.pos[static_cast<int64_t>(b) * s.pos_b + at] : static_cast<int64_t>(at);
-        const uint64_t turn = static_cast<uint64_t>(p) * a.turns[i];
-        const float rev = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-32f;
-        s_cs[id] = make_float2(__builtin_amdgcn_cosf(rev), __builtin_amdgcn_sinf(rev));
+                                           float *s_tab) {
+    const int per = a.D - a.half;  // pairs, then values that are not rotated
+    for (int id = static_cast<int>(threadIdx.x); id < n_tokens * per; id += kNormThreads) {
+        const uint32_t t = div_by(static_cast<uint32_t>(id), a.per), i = id - t * a.per.d;
+        float *c = s_tab + t * 2 * a.D, *sn = c + a.D;
+        if (static_cast<int>(i) < a.half) {
+            const uint32_t token = static_cast<uint32_t>(token0) + t;
+            const uint32_t b = div_by(token, s.len), at = token - b * s.len.d;
+            const int64_t p = s.pos ? s.pos[static_cast<int64_t>(b) * s.pos_b + at] : static_cast<int64_t>(at);
+            const uint64_t turn = static_cast<uint64_t>(p) * a.turns[i];
+            const float rev = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-32f;
+            const float cs = __builtin_amdgcn_cosf(rev), si = __builtin_amdgcn_sinf(rev);
+            const int e = INTER ? 2 * i : i, f = INTER ? e + 1 : e + a.half;
+            const float we = !BWD && s.w ? s.w[e] : 1.f, wf = !BWD && s.w ? s.w[f] : 1.f;
+            c[e] = cs * we;
+            c[f] = cs * wf;
+            sn[e] = BWD ? si : -si * wf;
+            sn[f] = BWD ? -si : si * we;
+        } else {
+            const int e = a.half + i;  // 2 half + (i - half)
+            c[e] = !BWD && s.w ? s.w[e] : 1.f;
+            sn[e] = 0.f;
+        }
     }
 }
 
-// The partner chunk of a half-split rotation, from the lane that holds it.
-template <int LPR>
-__device__ __forceinline__ u32x4 partner_chunk(u32x4 w, int src) {
-    u32x4 p;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = __shfl(w[j], src, 64);
-    return p;
-}
-
-// out = the rotation (sign +1) or inverse rotation (-1) of the lane's values
-// v; pv are the partner chunk's values (half-split pairs only).
+// The values v combined with their partners by the lane's factors.  pv: the
+// partner chunk's values (pairs (i, i + half)).
 template <int EPC, bool INTER>
-__device__ __forceinline__ void rotate(const float (&v)[EPC], const float (&pv)[EPC], const float2 *cs, int e0,
-                                       int half, float sign, float (&out)[EPC]) {
-    if constexpr (INTER) {
+__device__ __forceinline__ void combine(const float (&v)[EPC], const float (&pv)[EPC], const float *tab, int dim,
+                                        float (&out)[EPC]) {
 #pragma unroll
-        for (int i = 0; i < EPC; i += 2) {
-            const float2 t = cs[(e0 + i) >> 1];
-            const float sn = sign * t.y;
-            out[i] = fmaf(v[i], t.x, -(v[i + 1] * sn));
-            out[i + 1] = fmaf(v[i + 1], t.x, v[i] * sn);
-        }
-    } else {
-        const bool second = e0 >= half;
-        const int f = second ? e0 - half : e0;
+    for (int q = 0; q < EPC; q += 4) {
+        const f32v4 c = *reinterpret_cast<const f32v4 *>(tab + q), s = *reinterpret_cast<const f32v4 *>(tab + dim + q);
 #pragma unroll
-        for (int i = 0; i < EPC; ++i) {
-            const float2 t = cs[f + i];
-            const float sn = second ? sign * t.y : -sign * t.y;
-            out[i] = fmaf(v[i], t.x, pv[i] * sn);
-        }
+        for (int i = 0; i < 4; ++i) out[q + i] = fmaf(s[i], INTER ? v[(q + i) ^ 1] : pv[q + i], v[q + i] * c[i]);
     }
 }
 
@@ -98,6 +102,19 @@ __device__ __forceinline__ void store_chunk(void *base, int64_t element, const f
         for (int j = 0; j < 4; ++j) w[j] = pack2<T>(x[2 * j], x[2 * j + 1]);
     }
     *reinterpret_cast<u32x4 *>(static_cast<char *>(base) + element * T::kSize) = w;
+}
+
+// The partner chunk of a half-split rotation, from the lane that holds it.
+template <int LPR>
+__device__ __forceinline__ u32x4 partner_chunk(u32x4 w, int src) {
+    u32x4 p;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = __shfl(w[j], src, 64);
+    return p;
+}
+
+__device__ __forceinline__ bool same_strides(const HeadStrides &x, const HeadStrides &y) {
+    return x.b == y.b && x.t == y.t && x.h == y.h;
 }
 
 __device__ __forceinline__ int64_t head_offset(uint32_t token, uint32_t h, const NormSide &s, const HeadStrides &st) {
@@ -115,7 +132,7 @@ template <class T, int LPR, bool INTER, bool BWD>
 __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, int64_t block0) {
     using RL = RowLanes<T, LPR>;
     constexpr int EPC = RL::EPC;
-    __shared__ __align__(16) float2 s_cs[kTableBytes / sizeof(float2)];
+    __shared__ __align__(16) float s_tab[kTableBytes / sizeof(float)];
     const uint32_t bid = static_cast<uint32_t>(block0) + blockIdx.x;
     const int which = bid >= a.side[0].blocks ? 1 : 0;
     const NormSide &s = a.side[which];
@@ -123,15 +140,14 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, in
     const int tid = static_cast<int>(threadIdx.x);
     const int c = tid % LPR, e0 = c * EPC;
     const bool live = e0 < a.D;
-    const bool turned = live && e0 < 2 * a.half;
     // the lane of the chunk half a rotated block away
     const int lane = tid & 63, hc = a.half / EPC;
-    const int src = INTER || !turned ? lane : (c < hc ? lane + hc : lane - hc);
-    float w[EPC], pw[EPC], dw[EPC];
+    const int src = INTER || e0 >= 2 * a.half ? lane : (c < hc ? lane + hc : lane - hc);
+    const bool one_map = BWD ? same_strides(s.sx, s.sdy) && same_strides(s.sx, s.sdx) : same_strides(s.sx, s.sy);
+    float w[EPC], dw[EPC];
 #pragma unroll
     for (int i = 0; i < EPC; ++i) {
-        w[i] = s.w && live ? s.w[e0 + i] : (live ? 1.f : 0.f);
-        pw[i] = !INTER && turned && s.w ? s.w[(c < hc ? e0 + a.half : e0 - a.half) + i] : 1.f;
+        w[i] = BWD && s.w && live ? s.w[e0 + i] : 1.f;
         dw[i] = 0.f;
     }
     for (uint32_t tile = blk; tile < s.tiles; tile += s.blocks) {
@@ -140,58 +156,53 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, in
         const int n_rows = n_tokens * static_cast<int>(s.heads.d);
         for (int row0 = 0; row0 < n_rows; row0 += kUnroll * RL::kRows) {
             u32x4 raw[kUnroll], graw[kUnroll];
+            int64_t off[kUnroll];
             int at[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const int row = row0 + u * RL::kRows + tid / LPR;
                 const bool ok = live && row < n_rows;
                 const uint32_t t = div_by(static_cast<uint32_t>(row), s.heads), h = row - t * s.heads.d;
+                const uint32_t token = static_cast<uint32_t>(token0) + t;
                 at[u] = ok ? static_cast<int>(t) : -1;
+                off[u] = 0;
                 raw[u] = graw[u] = u32x4{0u, 0u, 0u, 0u};
                 if (ok) {
-                    const uint32_t token = static_cast<uint32_t>(token0) + t;
-                    raw[u] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(s.x) +
-                                                              (head_offset(token, h, s, s.sx) + e0) * T::kSize);
-                    if (BWD)
-                        graw[u] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(s.dy) +
-                                                                   (head_offset(token, h, s, s.sdy) + e0) * T::kSize);
+                    off[u] = head_offset(token, h, s, s.sx) + e0;
+                    raw[u] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(s.x) + off[u] * T::kSize);
+                    if constexpr (BWD) {
+                        if (!one_map) off[u] = head_offset(token, h, s, s.sdy) + e0;
+                        graw[u] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(s.dy) + off[u] * T::kSize);
+                    }
+                    if (!one_map) off[u] = head_offset(token, h, s, BWD ? s.sdx : s.sy) + e0;
                 }
             }
             if (row0 == 0) {
-                __syncthreads();  // the previous tile's table has been read
-                fill_table(a, s, token0, n_tokens, s_cs);
+                if (BWD) __syncthreads();  // the previous tile's factors have been read
+                fill_table<INTER, BWD>(a, s, token0, n_tokens, s_tab);
                 __syncthreads();
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const bool ok = at[u] >= 0;
-                const uint32_t row = static_cast<uint32_t>(row0 + u * RL::kRows + tid / LPR);
-                const uint32_t t = ok ? at[u] : 0, h = row - t * s.heads.d;
-                const uint32_t token = static_cast<uint32_t>(token0) + t;
-                const float2 *cs = s_cs + t * a.half;
-                float x[EPC];
+                const float *tab = s_tab + (ok ? at[u] : 0) * 2 * a.D + (live ? e0 : 0);
+                float x[EPC], v[EPC], pv[EPC];
                 unpack_chunk<T>(raw[u], x);
                 float q = 0.f;
 #pragma unroll
                 for (int i = 0; i < EPC; ++i) q = fmaf(x[i], x[i], q);
-                const float rstd = 1.f / sqrtf(fmaf(RL::sum(q), a.inv_d, a.eps));
+                const float rstd = rsqrtf(fmaf(RL::sum(q), a.inv_d, a.eps));
                 if constexpr (!BWD) {
-                    float n[EPC], pn[EPC], y[EPC];
-                    if constexpr (!INTER) unpack_chunk<T>(partner_chunk<LPR>(raw[u], src), pn);
+                    if constexpr (!INTER) unpack_chunk<T>(partner_chunk<LPR>(raw[u], src), pv);
+                    combine<EPC, INTER>(x, pv, tab, a.D, v);
 #pragma unroll
-                    for (int i = 0; i < EPC; ++i) {
-                        y[i] = n[i] = x[i] * rstd * w[i];
-                        if constexpr (!INTER) pn[i] = pn[i] * rstd * pw[i];
-                    }
-                    if (turned && ok) rotate<EPC, INTER>(n, pn, cs, e0, a.half, 1.f, y);
-                    if (ok) store_chunk<T>(s.y, head_offset(token, h, s, s.sy) + e0, y);
+                    for (int i = 0; i < EPC; ++i) v[i] *= rstd;
+                    if (ok) store_chunk<T>(s.y, off[u], v);
                 } else {
-                    float g[EPC], pg[EPC], v[EPC];
+                    float g[EPC];
                     unpack_chunk<T>(graw[u], g);
-                    if constexpr (!INTER) unpack_chunk<T>(partner_chunk<LPR>(graw[u], src), pg);
-#pragma unroll
-                    for (int i = 0; i < EPC; ++i) v[i] = g[i];
-                    if (turned && ok) rotate<EPC, INTER>(g, pg, cs, e0, a.half, -1.f, v);
+                    if constexpr (!INTER) unpack_chunk<T>(partner_chunk<LPR>(graw[u], src), pv);
+                    combine<EPC, INTER>(g, pv, tab, a.D, v);
                     float dot = 0.f;
 #pragma unroll
                     for (int i = 0; i < EPC; ++i) {
@@ -203,7 +214,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, in
                     const float mean = RL::sum(dot) * a.inv_d;
 #pragma unroll
                     for (int i = 0; i < EPC; ++i) v[i] = rstd * fmaf(-mean, x[i], v[i]);
-                    if (ok) store_chunk<T>(s.dx, head_offset(token, h, s, s.sdx) + e0, v);
+                    if (ok) store_chunk<T>(s.dx, off[u], v);
                 }
             }
         }
@@ -212,7 +223,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, in
         if (!s.dw) return;
         // Sum of the workgroup's row groups, in their order.
         __syncthreads();
-        float *sum = reinterpret_cast<float *>(s_cs);  // [kRows][LPR * EPC]: 8 KB at most
+        float *sum = s_tab;  // [kRows][LPR * EPC]: 8 KB at most
 #pragma unroll
         for (int i = 0; i < EPC; ++i) sum[(tid / LPR) * (LPR * EPC) + e0 + i] = dw[i];
         __syncthreads();
@@ -257,7 +268,8 @@ void plan(NormArgs &a, int32_t dtype, bool bwd) {
     while (lanes < chunks) lanes *= 2;
     const uint32_t heads = a.side[a.side[1].tokens > a.side[0].tokens ? 1 : 0].heads.d;
     uint32_t tile = kUnroll * (kNormThreads / lanes) / heads;
-    const uint32_t most = a.half > 0 ? kTableBytes / (8u * a.half) : 64u;
+    const uint32_t most = kTableBytes / (8u * a.D);
+    a.per = fast_div(static_cast<uint32_t>(a.D - a.half));
     tile = tile < 1 ? 1 : tile;
     a.tile = tile > most ? most : tile;
     for (NormSide &s : a.side) {

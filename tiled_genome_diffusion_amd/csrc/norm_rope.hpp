@@ -27,6 +27,7 @@ struct NormArgs {
     NormSide side[2];        // queries, keys (tokens = 0: absent)
     uint64_t turns[kMaxPairs2];  // 2^64 * (angle per position of pair i) / 2 pi, modulo 2^64
     int32_t D, half;         // head size, rotated pairs
+    FastDiv per;             // D - half: pairs and values that are not rotated
     uint32_t tile;           // tokens a workgroup takes at a time
     float eps, inv_d;
 };
