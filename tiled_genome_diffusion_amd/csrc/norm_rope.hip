@@ -21,7 +21,7 @@ namespace pc {
 namespace {
 
 constexpr int kNormThreads = 256;
-// Factors of a workgroup's tokens in LDS.
+// Most LDS for the factors of a workgroup's tokens; a launch takes what its tile needs.
 constexpr int kTableBytes = 32768;
 
 // A head's row is held by LPR lanes of 16 bytes each, the lane's chunk the
@@ -124,15 +124,17 @@ __device__ __forceinline__ int64_t head_offset(uint32_t token, uint32_t h, const
 
 // Forward and, with BWD, the gradients.  A workgroup takes tiles of `tile`
 // tokens, all heads of each; queries' workgroups come first in the grid.  The
-// rows of a tile are taken kUnroll per lane at a time, all loads ahead of the
+// rows of a tile are taken U per lane at a time, all loads ahead of the
 // arithmetic (and the first ones ahead of the tile's table).
-constexpr int kUnroll = 4;
+template <bool BWD>
+constexpr int kUnroll = BWD ? 2 : 4;
 
 template <class T, int LPR, bool INTER, bool BWD>
 __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, int64_t block0) {
     using RL = RowLanes<T, LPR>;
     constexpr int EPC = RL::EPC;
-    __shared__ __align__(16) float s_tab[kTableBytes / sizeof(float)];
+    extern __shared__ __align__(16) float s_tab[];
+    constexpr int U = kUnroll<BWD>;
     const uint32_t bid = static_cast<uint32_t>(block0) + blockIdx.x;
     const int which = bid >= a.side[0].blocks ? 1 : 0;
     const NormSide &s = a.side[which];
@@ -154,12 +156,12 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, in
         const int64_t token0 = static_cast<int64_t>(tile) * a.tile;
         const int n_tokens = static_cast<int>(s.tokens - token0 < a.tile ? s.tokens - token0 : a.tile);
         const int n_rows = n_tokens * static_cast<int>(s.heads.d);
-        for (int row0 = 0; row0 < n_rows; row0 += kUnroll * RL::kRows) {
-            u32x4 raw[kUnroll], graw[kUnroll];
-            int64_t off[kUnroll];
-            int at[kUnroll];
+        for (int row0 = 0; row0 < n_rows; row0 += U * RL::kRows) {
+            u32x4 raw[U], graw[U];
+            int64_t off[U];
+            int at[U];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int row = row0 + u * RL::kRows + tid / LPR;
                 const bool ok = live && row < n_rows;
                 const uint32_t t = div_by(static_cast<uint32_t>(row), s.heads), h = row - t * s.heads.d;
@@ -183,7 +185,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_rope(const NormArgs a, in
                 __syncthreads();
             }
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const bool ok = at[u] >= 0;
                 const float *tab = s_tab + (ok ? at[u] : 0) * 2 * a.D + (live ? e0 : 0);
                 float x[EPC], v[EPC], pv[EPC];
@@ -260,14 +262,14 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const NormArgs a, int64_t bloc
 
 constexpr uint32_t kBwdBlocks = 1024;  // of a side: its tiles are dealt to at most this many workgroups
 
-// Tokens per tile: the rows a workgroup holds in kUnroll steps (of the side
+// Tokens per tile: the rows a workgroup holds at once (of the side
 // that has more tokens), as many as the table holds.
 void plan(NormArgs &a, int32_t dtype, bool bwd) {
     const uint32_t chunks = static_cast<uint32_t>(a.D) * (dtype == kF32 ? 4 : 2) / 16;
     uint32_t lanes = 4;
     while (lanes < chunks) lanes *= 2;
     const uint32_t heads = a.side[a.side[1].tokens > a.side[0].tokens ? 1 : 0].heads.d;
-    uint32_t tile = kUnroll * (kNormThreads / lanes) / heads;
+    uint32_t tile = (bwd ? kUnroll<true> : kUnroll<false>) * (kNormThreads / lanes) / heads;
     const uint32_t most = kTableBytes / (8u * a.D);
     a.per = fast_div(static_cast<uint32_t>(a.D - a.half));
     tile = tile < 1 ? 1 : tile;
@@ -299,10 +301,13 @@ void for_row_lanes(int32_t dtype, int32_t dim, bool interleaved, F &&f) {
 template <bool BWD>
 hipError_t launch(const NormArgs &a, int32_t dtype, bool interleaved, hipStream_t stream) {
     const int64_t blocks = static_cast<int64_t>(a.side[0].blocks) + a.side[1].blocks;
+    const uint32_t chunk = 16u / (dtype == kF32 ? 4u : 2u);
+    const uint32_t table = a.tile * 8u * static_cast<uint32_t>(a.D), sums = BWD ? kNormThreads * chunk * 4u : 0u;
+    const uint32_t lds = table > sums ? table : sums;
     return launch_slices(blocks, kNormThreads, [&](int64_t first, uint32_t count) {
         for_row_lanes(dtype, a.D, interleaved, [&](auto type, auto lanes, auto inter) {
             k_norm_rope<decltype(type), decltype(lanes)::value, decltype(inter)::value, BWD>
-                <<<count, kNormThreads, 0, stream>>>(a, first);
+                <<<count, kNormThreads, lds, stream>>>(a, first);
         });
     });
 }
