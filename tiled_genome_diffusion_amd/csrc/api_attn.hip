@@ -120,6 +120,16 @@ pc_status check_attention(const pc_attention *a, bool backward, pc::AttnArgs *ou
     r.rep = pc::fast_div(static_cast<uint32_t>(rep));
     r.len_q = pc::fast_div(a->len_q > 0 ? static_cast<uint32_t>(a->len_q) : 1u);
     r.heads_kv = pc::fast_div(static_cast<uint32_t>(a->heads_kv));
+    // Maps that follow each other at len_q token strides are one run of tokens.
+    r.merged = 1;
+    for (const auto &x : t)
+        if (x.needed && x.query && a->group > 1 && a->len_q > 1 && x.to->b != a->len_q * x.to->t) r.merged = 0;
+    if (r.merged && rows > 0) {
+        r.len_q = pc::fast_div(static_cast<uint32_t>(a->group) * static_cast<uint32_t>(a->len_q));
+        if (a->len_q == 1)
+            for (const auto &x : t)
+                if (x.needed && x.query) x.to->t = x.to->b;
+    }
     r.scale = a->scale;
     r.scale_log2 = a->scale * pc::kLog2e;
     *out = r;

@@ -61,6 +61,7 @@ struct AttnArgs {
     int32_t n_kv, group, Lq, Lk, H, Hk, D;
     uint32_t rows;          // M
     uint32_t split_tiles;   // staged tiles per split
+    int32_t merged;         // the maps of a state follow each other at len_q token strides in every query tensor
     float scale;            // softmax scale
     float scale_log2;       // scale log2(e)
 };
@@ -298,6 +299,9 @@ struct Loader {
 #pragma unroll
         for (int i = 0; i < TL::NCH; ++i) p[i] += bytes;
     }
+    // Query rows row0, row0 + 1, ... of one key head; those past the last row are not looked at.
+    __device__ __forceinline__ void point_rows(const void *base, int64_t off, const HeadStrides &s, int64_t row0,
+                                               const AttnArgs &a);
     // Starts the loads of the rows whose bit of `valid` is set (all: every bit of the tile is).
     __device__ __forceinline__ void start(char *tile, uint64_t valid, bool all) const {
         char *at = tile + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * 1024;
@@ -358,6 +362,14 @@ __device__ __forceinline__ int64_t row_offset(uint32_t row, const AttnArgs &a, c
     const uint32_t m = div_by(t, a.len_q), i = t - m * a.len_q.d;
     return static_cast<int64_t>(m) * s.b + static_cast<int64_t>(i) * s.t + static_cast<int64_t>(hr) * s.h;
 }
+template <class T, int DP>
+__device__ __forceinline__ void Loader<T, DP>::point_rows(const void *base, int64_t off, const HeadStrides &s,
+                                                          int64_t row0, const AttnArgs &a) {
+#pragma unroll
+    for (int i = 0; i < TL::NCH; ++i)
+        p[i] = static_cast<const char *>(base) +
+               (off + row_offset(static_cast<uint32_t>(row0 + row(i)), a, s) + chunk(i) * TL::EPC) * TL::kSize;
+}
 __device__ __forceinline__ int64_t pair_offset(uint32_t r, uint32_t j, const AttnArgs &a, const HeadStrides &s) {
     return static_cast<int64_t>(r) * a.group * s.b + static_cast<int64_t>(j) * a.rep.d * s.h;
 }
@@ -395,6 +407,13 @@ void for_dtype_dim(int32_t dtype, int32_t dim, F &&f) {
     if (dtype == kBf16) dims(Bf16{});
     else if (dtype == kF16) dims(F16{});
     else dims(F32{});
+}
+
+// Row blocks of a wavefront: two where that still leaves two workgroups per
+// compute unit (each K and V fragment read from LDS then serves two products).
+inline int attn_row_blocks(const AttnArgs &a, int32_t dtype) {
+    const int64_t pairs = static_cast<int64_t>(a.n_kv) * a.Hk;
+    return dtype != kF32 && a.D <= 64 && pairs * ((static_cast<int64_t>(a.rows) + 255) / 256) >= 512 ? 2 : 1;
 }
 
 // How a grid of (pairs) x (tiles of the parallel axis) is split over the long

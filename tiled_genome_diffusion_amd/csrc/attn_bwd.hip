@@ -10,9 +10,9 @@
 namespace pc {
 namespace {
 
-// dQ (and delta, for the kernel below): 4 wavefronts of 32 rows, keys and
-// values in LDS tiles, as the forward.
-template <class T, int DP, bool SPLIT>
+// dQ (and delta, for the kernel below): 4 wavefronts of NR blocks of 32 rows,
+// keys and values in LDS tiles, as the forward.
+template <class T, int DP, int NR, bool SPLIT>
 __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k_attn_dq(const AttnArgs a, int64_t block0) {
     using TL = Tile<T, DP>;
     __shared__ __align__(16) char s_kv[2][2 * TL::kBytes];
@@ -23,33 +23,38 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
     const uint32_t pair = div_by(ps, a.n_split), split = ps - pair * a.n_split.d;
     const uint32_t r = div_by(pair, a.heads_kv), j = pair - r * a.heads_kv.d;
 
-    const uint32_t row = rt * (kAttnWaves * 32) + wave * 32 + col;
-    const bool row_ok = row < a.rows;
-    u32x4 qf[TL::FR], gf[TL::FR];
-    float delta = 0.f, lse2 = INFINITY;  // rows past the end: P = 0
-    {
-        const int64_t offq = pair_offset(r, j, a, a.sq) + (row_ok ? row_offset(row, a, a.sq) : 0);
-        const int64_t offg = pair_offset(r, j, a, a.sdo) + (row_ok ? row_offset(row, a, a.sdo) : 0);
-        const int64_t offo = pair_offset(r, j, a, a.so) + (row_ok ? row_offset(row, a, a.so) : 0);
+    const uint32_t row0 = (rt * kAttnWaves + wave) * (NR * 32) + col;  // and row0 + 32
+    const bool idle = row0 - col >= a.rows;                            // no row of this wavefront exists
+    u32x4 qf[NR][TL::FR], gf[NR][TL::FR];
+    f32x16 dq[NR][TL::DT];
+    float delta[NR], lse2[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const uint32_t row = row0 + 32 * n;
+        const bool ok = row < a.rows;
+        const int64_t offq = pair_offset(r, j, a, a.sq) + (ok ? row_offset(row, a, a.sq) : 0);
+        const int64_t offg = pair_offset(r, j, a, a.sdo) + (ok ? row_offset(row, a, a.sdo) : 0);
+        const int64_t offo = pair_offset(r, j, a, a.so) + (ok ? row_offset(row, a, a.so) : 0);
+        delta[n] = 0.f;
+        lse2[n] = INFINITY;  // rows past the end: P = 0
 #pragma unroll
         for (int f = 0; f < TL::FR; ++f) {
-            qf[f] = load_chunk<T>(a.q, offq, 2 * f + half, a.D, row_ok);
-            gf[f] = load_chunk<T>(a.dout, offg, 2 * f + half, a.D, row_ok);
+            qf[n][f] = load_chunk<T>(a.q, offq, 2 * f + half, a.D, ok);
+            gf[n][f] = load_chunk<T>(a.dout, offg, 2 * f + half, a.D, ok);
             float g[TL::EPC], o[TL::EPC];
-            unpack_chunk<T>(gf[f], g);
-            unpack_chunk<T>(load_chunk<T>(a.o_in, offo, 2 * f + half, a.D, row_ok), o);
+            unpack_chunk<T>(gf[n][f], g);
+            unpack_chunk<T>(load_chunk<T>(a.o_in, offo, 2 * f + half, a.D, ok), o);
 #pragma unroll
-            for (int i = 0; i < TL::EPC; ++i) delta = fmaf(g[i], o[i], delta);
+            for (int i = 0; i < TL::EPC; ++i) delta[n] = fmaf(g[i], o[i], delta[n]);
         }
-        delta += other_half(delta);
-        if (row_ok) lse2 = a.lse[lse_index(r, j, row, a)] * kLog2e;
-        if (row_ok && half == 0 && split == 0) a.delta[static_cast<int64_t>(pair) * a.rows + row] = delta;
+        delta[n] += other_half(delta[n]);
+        if (ok) lse2[n] = a.lse[lse_index(r, j, row, a)] * kLog2e;
+        if (ok && half == 0 && split == 0) a.delta[static_cast<int64_t>(pair) * a.rows + row] = delta[n];
+#pragma unroll
+        for (int d = 0; d < TL::DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dq[n][d][i] = 0.f;
     }
-    f32x16 dq[TL::DT];
-#pragma unroll
-    for (int d = 0; d < TL::DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dq[d][i] = 0.f;
 
     const int n_keys = keys_of(r, a);
     const int first = static_cast<int>(split * a.split_tiles) * TL::BN;
@@ -88,44 +93,66 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
             gk.start(s_kv[buf ^ 1], next, next == kAll);
             gv.start(s_kv[buf ^ 1] + TL::kBytes, next, next == kAll);
         }
+        const uint64_t here = idle ? 0 : valid;
+        valid = next;
 #pragma unroll
         for (int t = 0; t < TL::SUB; ++t) {
-            const uint32_t live = static_cast<uint32_t>(valid >> (32 * t));
+            const uint32_t live = static_cast<uint32_t>(here >> (32 * t));
             if (live == 0) continue;
-            f32x16 s, g;
+            f32x16 s[NR], g[NR];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = g[i] = 0.f;
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[n][i] = g[n][i] = 0.f;
 #pragma unroll
             for (int f = 0; f < TL::FR; ++f) {
-                s = mma<T>(TL::frag(s_k, t * 32 + col, f, half), qf[f], s);
-                g = mma<T>(TL::frag(s_v, t * 32 + col, f, half), gf[f], g);
+                const u32x4 kf = TL::frag(s_k, t * 32 + col, f, half), vf = TL::frag(s_v, t * 32 + col, f, half);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    s[n] = mma<T>(kf, qf[n][f], s[n]);
+                    g[n] = mma<T>(vf, gf[n][f], g[n]);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = exp2_hw(fmaf(s[i], a.scale_log2, -lse2)) * (g[i] - delta);
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[n][i] = exp2_hw(fmaf(s[n][i], a.scale_log2, -lse2[n])) * (g[n][i] - delta[n]);
             if (live != 0xFFFFFFFFu) {
                 const uint32_t bits = live >> (4 * half);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (!((bits >> (8 * (i / 4) + i % 4)) & 1)) s[i] = 0.f;
+                    if (!((bits >> (8 * (i / 4) + i % 4)) & 1))
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) s[n][i] = 0.f;
             }
 #pragma unroll
             for (int b = 0; b < TL::NB; ++b) {
-                const u32x4 p = pack_frag<T>(s, b);
+                u32x4 p[NR];
 #pragma unroll
-                for (int d = 0; d < TL::DT; ++d)
-                    dq[d] = mma<T>(TL::frag_t(s_k, t * 32 + b * 2 * TL::EPC, d * 32, lane), p, dq[d]);
+                for (int n = 0; n < NR; ++n) p[n] = pack_frag<T>(s[n], b);
+#pragma unroll
+                for (int d = 0; d < TL::DT; ++d) {
+                    const u32x4 kf = TL::frag_t(s_k, t * 32 + b * 2 * TL::EPC, d * 32, lane);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) dq[n][d] = mma<T>(kf, p[n], dq[n][d]);
+                }
             }
         }
-        valid = next;
     }
-    const int64_t off = pair_offset(r, j, a, a.sdq) + (row_ok ? row_offset(row, a, a.sdq) : 0);
-    const int64_t slot = (static_cast<int64_t>(split) * a.n_kv * a.Hk + pair) * a.rows + row;
 #pragma unroll
-    for (int d = 0; d < TL::DT; ++d) {
-        if constexpr (SPLIT)
-            store_row_block<F32>(a.part, slot * a.D, dq[d], a.scale, d * 32, half, a.D, row_ok);
-        else
-            store_row_block<T>(a.dq, off, dq[d], a.scale, d * 32, half, a.D, row_ok);
+    for (int n = 0; n < NR; ++n) {
+        const uint32_t row = row0 + 32 * n;
+        const bool ok = row < a.rows;
+        const int64_t off = pair_offset(r, j, a, a.sdq) + (ok ? row_offset(row, a, a.sdq) : 0);
+        const int64_t slot = (static_cast<int64_t>(split) * a.n_kv * a.Hk + pair) * a.rows + row;
+#pragma unroll
+        for (int d = 0; d < TL::DT; ++d) {
+            if constexpr (SPLIT)
+                store_row_block<F32>(a.part, slot * a.D, dq[n][d], a.scale, d * 32, half, a.D, ok);
+            else
+                store_row_block<T>(a.dq, off, dq[n][d], a.scale, d * 32, half, a.D, ok);
+        }
     }
 }
 
@@ -136,7 +163,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
 // dK^T = Q^T dS as they stand.  A key that is not attended is a column of its
 // own, dropped at the end; its K and V are zero on the way.
 template <class T, int DP, bool SPLIT>
-__global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k_attn_dkv(const AttnArgs a, int64_t block0) {
+__global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 : 1)) void k_attn_dkv(const AttnArgs a, int64_t block0) {
     using TL = Tile<T, DP>;
     __shared__ __align__(16) char s_qg[2][2 * TL::kBytes];  // Q tile, dO tile; two of each
     __shared__ __align__(16) float s_stat[2][2 * TL::BN];   // lse log2(e), delta of the tile's rows
@@ -152,6 +179,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k
     const int key = static_cast<int>(kt) * (kAttnWaves * 32) + wave * 32 + col;
     bool key_ok = key < n_keys;
     if (a.key_mask && key_ok) key_ok = a.key_mask[static_cast<int64_t>(r) * a.Lk + key] != 0;
+    const bool idle = !__any(key_ok);  // no key of this wavefront is attended
     u32x4 kf[TL::FR], vf[TL::FR];
     {
         const int64_t offk = static_cast<int64_t>(r) * a.sk.b + static_cast<int64_t>(j) * a.sk.h + (key_ok ? key * a.sk.t : 0);
@@ -177,22 +205,24 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k
     constexpr uint64_t kAll = TL::BN == 64 ? ~0ull : 0xFFFFFFFFull;
     Loader<T, DP> gq, gg;
     float g_lse = 0.f, g_delta = 0.f;
+    // With whole groups of rep rows in a tile and the maps in one run, a tile's
+    // rows lie a constant step after the last tile's.
+    const bool steady = a.merged && TL::BN % a.rep.d == 0;
+    const int64_t tokens = TL::BN / a.rep.d;  // of a tile, when steady
+    const float *g_lse_at = nullptr;
+    const auto point = [&](int64_t row0) {
+        gq.point_rows(a.q, baseq, a.sq, row0, a);
+        gg.point_rows(a.dout, baseg, a.sdo, row0, a);
+        g_lse_at = a.lse + lse_index(r, j, static_cast<uint32_t>(row0 + tid), a);
+    };
     const auto start = [&](int64_t row0, int b) {
         const bool all = row0 + TL::BN <= end;
         const uint64_t valid = all ? kAll : (1ull << (end - row0)) - 1;
-#pragma unroll
-        for (int i = 0; i < TL::NCH; ++i) {
-            const int64_t row = row0 + Loader<T, DP>::row(i);
-            const uint32_t n = static_cast<uint32_t>(row < end ? row : row0);
-            const int c = Loader<T, DP>::chunk(i) * TL::EPC;
-            gq.p[i] = static_cast<const char *>(a.q) + (baseq + row_offset(n, a, a.sq) + c) * T::kSize;
-            gg.p[i] = static_cast<const char *>(a.dout) + (baseg + row_offset(n, a, a.sdo) + c) * T::kSize;
-        }
         gq.start(s_qg[b], valid, all);
         gg.start(s_qg[b] + TL::kBytes, valid, all);
         if (tid < TL::BN) {
             const bool ok = row0 + tid < end;
-            g_lse = ok ? a.lse[lse_index(r, j, static_cast<uint32_t>(row0 + tid), a)] * kLog2e : INFINITY;
+            g_lse = ok ? *g_lse_at * kLog2e : INFINITY;
             g_delta = ok ? delta[row0 + tid] : 0.f;
         }
     };
@@ -209,6 +239,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k
         }
         gq.init(a.D);
         gg.init(a.D);
+        point(first);
         start(first, 0);
     }
     int buf = 0;
@@ -218,12 +249,28 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k
         __syncthreads();  // the tile is here, and every wavefront has left the other one
         const char *s_q = s_qg[buf], *s_g = s_qg[buf] + TL::kBytes;
         const float *stat = s_stat[buf];
-        if (row0 + TL::BN < end) start(row0 + TL::BN, buf ^ 1);
+        if (row0 + TL::BN < end) {
+            if (steady) {
+                gq.advance(tokens * a.sq.t * T::kSize);
+                gg.advance(tokens * a.sdo.t * T::kSize);
+                g_lse_at += tokens * a.H;
+            } else {
+                point(row0 + TL::BN);
+            }
+            start(row0 + TL::BN, buf ^ 1);
+        }
+        if (idle) continue;
 #pragma unroll
         for (int t = 0; t < TL::SUB; ++t) {
             f32x16 s, g;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = g[i] = 0.f;
+            for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const f32v4 de = *reinterpret_cast<const f32v4 *>(stat + TL::BN + t * 32 + 2 * i + 4 * half);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) g[i + n] = -de[n];  // dP - delta
+            }
 #pragma unroll
             for (int f = 0; f < TL::FR; ++f) {
                 s = mma<T>(TL::frag(s_q, t * 32 + col, f, half), kf[f], s);
@@ -232,11 +279,10 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 192 ? 2 : 1)) void k
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
                 const f32v4 ls = *reinterpret_cast<const f32v4 *>(stat + t * 32 + 2 * i + 4 * half);
-                const f32v4 de = *reinterpret_cast<const f32v4 *>(stat + TL::BN + t * 32 + 2 * i + 4 * half);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     s[i + n] = exp2_hw(fmaf(s[i + n], a.scale_log2, -ls[n]));
-                    g[i + n] = s[i + n] * (g[i + n] - de[n]);
+                    g[i + n] *= s[i + n];
                 }
             }
 #pragma unroll
@@ -300,13 +346,15 @@ __global__ __launch_bounds__(256) void k_attn_sum(const AttnArgs a, const float 
 
 struct BwdPlan {
     AttnPlan q, kv;
+    int nr;  // row blocks of a wavefront in dQ
     int64_t pairs, bytes_delta, bytes_q, bytes_kv;
 };
 BwdPlan bwd_plan(const AttnArgs &a, int32_t dtype) {
     const int64_t bn = dtype == kF32 ? 32 : 64;
     BwdPlan p;
     p.pairs = static_cast<int64_t>(a.n_kv) * a.Hk;
-    p.q = attn_plan(p.pairs, (static_cast<int64_t>(a.rows) + 127) / 128, (a.Lk + bn - 1) / bn, 4);
+    p.nr = attn_row_blocks(a, dtype);
+    p.q = attn_plan(p.pairs, (static_cast<int64_t>(a.rows) + 128 * p.nr - 1) / (128 * p.nr), (a.Lk + bn - 1) / bn, 4);
     p.kv = attn_plan(p.pairs, (static_cast<int64_t>(a.Lk) + 127) / 128, (a.rows + bn - 1) / bn, 4);
     p.bytes_delta = round16(p.pairs * a.rows * 4);
     p.bytes_q = p.q.n_split > 1 ? p.q.n_split * p.pairs * a.rows * a.D * 4 : 0;
@@ -345,10 +393,13 @@ hipError_t launch_attn_bwd(AttnArgs a, int32_t dtype, char *workspace, hipStream
             for_dtype_dim(dtype, a.D, [&](auto type, auto dim) {
                 using T = decltype(type);
                 constexpr int DP = decltype(dim)::value;
+                if constexpr (T::kSize == 2 && DP <= 64) {
+                    if (p.nr == 2) return k_attn_dq<T, DP, 2, false><<<count, kAttnThreads, 0, stream>>>(a, first);
+                }
                 if (p.q.n_split > 1)
-                    k_attn_dq<T, DP, true><<<count, kAttnThreads, 0, stream>>>(a, first);
+                    k_attn_dq<T, DP, 1, true><<<count, kAttnThreads, 0, stream>>>(a, first);
                 else
-                    k_attn_dq<T, DP, false><<<count, kAttnThreads, 0, stream>>>(a, first);
+                    k_attn_dq<T, DP, 1, false><<<count, kAttnThreads, 0, stream>>>(a, first);
             });
         });
         if (e == hipSuccess && p.q.n_split > 1) e = sum_splits<true>(a, a.part, a.dq, a.sdq, dtype, a.rows, stream);

@@ -33,6 +33,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
     const uint32_t r = div_by(pair, a.heads_kv), j = pair - r * a.heads_kv.d;
 
     const uint32_t row0 = (rt * kAttnWaves + wave) * (NR * 32) + col;  // and row0 + 32
+    const bool idle = row0 - col >= a.rows;                            // no row of this wavefront exists
     u32x4 qf[NR][TL::FR];
     f32x16 o[NR][TL::DT];
     float m[NR], l[NR];
@@ -89,7 +90,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
             gk.start(s_kv[buf ^ 1], next, next == kAll);
             gv.start(s_kv[buf ^ 1] + TL::kBytes, next, next == kAll);
         }
-        if (valid != 0) {
+        if (valid != 0 && !idle) {
             f32x16 s[NR][TL::SUB];
 #pragma unroll
             for (int t = 0; t < TL::SUB; ++t) {
@@ -252,16 +253,9 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int32_t dty
 
 }  // namespace
 
-// Row blocks of a wavefront: two where that still leaves two workgroups per
-// compute unit (each K and V fragment read from LDS then serves two products).
-int row_blocks(const AttnArgs &a, int32_t dtype) {
-    const int64_t pairs = static_cast<int64_t>(a.n_kv) * a.Hk;
-    return dtype != kF32 && a.D <= 64 && pairs * ((static_cast<int64_t>(a.rows) + 255) / 256) >= 512 ? 2 : 1;
-}
-
 AttnPlan attn_fwd_plan(const AttnArgs &a, int32_t dtype) {
     const int bn = dtype == kF32 ? 32 : 64;
-    const int64_t rows = 128 * row_blocks(a, dtype);
+    const int64_t rows = 128 * attn_row_blocks(a, dtype);
     return attn_plan(static_cast<int64_t>(a.n_kv) * a.Hk, (a.rows + rows - 1) / rows, (a.Lk + bn - 1) / bn, 4);
 }
 
@@ -283,7 +277,7 @@ hipError_t launch_attn_fwd(AttnArgs a, int32_t dtype, char *workspace, hipStream
         a.part_ml = reinterpret_cast<float *>(workspace + round16(p.n_split * pairs * a.rows * a.D * 4));
     }
     const int64_t blocks = pairs * p.n_split * p.n_tiles;
-    const int nr = row_blocks(a, dtype);
+    const int nr = attn_row_blocks(a, dtype);
     const hipError_t e = launch_slices(blocks, kAttnThreads, [&](int64_t first, uint32_t count) {
         for_dtype_dim(dtype, a.D, [&](auto type, auto dim) {
             using T = decltype(type);
