@@ -208,12 +208,14 @@ struct Tile {
     static constexpr int kBytes = BN * ROWB;
 
     __device__ static __forceinline__ int swz(int row, int c) {
-        constexpr int s = (CH == 4 || CH == 12) ? 1 : 0;  // rows of 64 and 192 bytes: bank parity from row bit 0
-        const int r = row >> s;
-        if constexpr (CH % 8 == 0)
-            return c ^ ((r & 1) | ((r & 4) >> 1) | ((r & 2) << 1));
-        else
-            return c ^ (r & 3);
+        if constexpr (CH % 16 == 0 && kSize == 4)  // rows of whole bank widths (256 bytes); frag_t reads rows 4 apart
+            return c ^ ((row & 4) << 1 | ((row >> 1) & 4) | (row & 3));
+        else if constexpr (CH % 16 == 0)
+            return c ^ ((row & 3) << 2 | ((row >> 2) & 3));
+        else if constexpr (CH % 8 == 0)  // of 128 bytes and odd multiples: the row's lowest bit moves the banks
+            return c ^ ((row & 2) << 1 | ((row >> 1) & 2) | ((row >> 3) & 1));
+        else                             // of 64 and 192: its two lowest bits do
+            return c ^ ((row >> 2) & 3);
     }
     __device__ static __forceinline__ int at(int row, int c) { return row * ROWB + swz(row, c) * 16; }
 
