@@ -9,15 +9,23 @@
 // 8 heads are the same product with another M, and K and V are staged once for
 // all of them.
 //
-// Matrix operands.  A fragment is 16 bytes per lane: lane l holds row (or
-// column) l & 31 and, of a block of 2 EPC contraction values, the EPC of half
-// l >> 5 (EPC = 8 values of 16 bits, one 32x32x16 instruction; 4 floats, four
-// 32x32x2 instructions).  The accumulator of a 32x32 product holds in register
+// Matrix operands.  A fragment is 8 values per lane: lane l holds row (or
+// column) l & 31 and, of a block of 16 contraction values, the 8 of half
+// l >> 5.  The accumulator of a 32x32 product holds in register
 // r of lane l: row 8 (r / 4) + 4 (l >> 5) + r % 4, column l & 31.  A product's
 // accumulator, rounded, is therefore the second operand of the next product as
 // it stands (contraction over its rows, in this order): probabilities never
 // pass through LDS.  The first operand of that product is read from the same
-// row-major tile, transposed on the way (ds_read_b64_tr_b16 for 16-bit types).
+// row-major tile, transposed on the way (ds_read_b64_tr_b16).
+//
+// float32.  A float is the exact sum of three bfloat16 values of 8 bits each,
+// x = x0 + x1 + x2 (cut off, not rounded, so no part overflows).  A product of
+// two such numbers is taken as the six products whose parts' orders add to two
+// at most; what is left out is below 2^-23 of the product, the size of
+// float32's own rounding.  Six bfloat16 products of 32x32x16 take 192 cycles a
+// SIMD where eight float32 ones of 32x32x2 take 512.  An infinite query or key
+// value counts as the largest bfloat16 (a score of -inf still gets no weight);
+// an infinite value or gradient gives NaN.
 #pragma once
 
 #include <type_traits>
@@ -69,13 +77,13 @@ struct AttnArgs {
 // Element types, as the ABI numbers them (pc.h).
 constexpr int32_t kF32 = 0, kBf16 = 1, kF16 = 2;
 struct Bf16 {
-    static constexpr int kSize = 2;
+    static constexpr int kSize = 2, kPlanes = 1;
 };
 struct F16 {
-    static constexpr int kSize = 2;
+    static constexpr int kSize = 2, kPlanes = 1;
 };
 struct F32 {
-    static constexpr int kSize = 4;
+    static constexpr int kSize = 4, kPlanes = 3;
 };
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -86,24 +94,59 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
+// 8 values of one lane as a matrix operand; float32 in three parts.
 template <class T>
-__device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c);
-template <>
-__device__ __forceinline__ f32x16 mma<Bf16>(u32x4 a, u32x4 b, f32x16 c) {
+struct Frag {
+    u32x4 p[T::kPlanes];
+};
+
+__device__ __forceinline__ f32x16 mma_bf16(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
 }
-template <>
-__device__ __forceinline__ f32x16 mma<F16>(u32x4 a, u32x4 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
-                                                  0);
+template <class T>
+__device__ __forceinline__ f32x16 mma(const Frag<T> &a, const Frag<T> &b, f32x16 c) {
+    if constexpr (std::is_same_v<T, F16>) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a.p[0]),
+                                                      __builtin_bit_cast(f16x8, b.p[0]), c, 0, 0, 0);
+    } else if constexpr (T::kPlanes == 3) {  // smallest first
+        c = mma_bf16(a.p[2], b.p[0], c);
+        c = mma_bf16(a.p[1], b.p[1], c);
+        c = mma_bf16(a.p[0], b.p[2], c);
+        c = mma_bf16(a.p[1], b.p[0], c);
+        c = mma_bf16(a.p[0], b.p[1], c);
+        return mma_bf16(a.p[0], b.p[0], c);
+    } else {
+        return mma_bf16(a.p[0], b.p[0], c);
+    }
 }
-template <>
-__device__ __forceinline__ f32x16 mma<F32>(u32x4 a, u32x4 b, f32x16 c) {
-    const f32v4 x = __builtin_bit_cast(f32v4, a), y = __builtin_bit_cast(f32v4, b);
+
+// The three parts of two floats, packed.
+__device__ __forceinline__ void split3(float x, float y, uint32_t &h, uint32_t &m, uint32_t &l) {
+    constexpr uint32_t kTop = 0xFFFF0000u, kUpper = 0x07060302u;  // upper halves of two dwords
+    const uint32_t xb = __float_as_uint(x), yb = __float_as_uint(y);
+    const float xr = x - __uint_as_float(xb & kTop), yr = y - __uint_as_float(yb & kTop);
+    const uint32_t xm = __float_as_uint(xr), ym = __float_as_uint(yr);
+    const float xl = xr - __uint_as_float(xm & kTop), yl = yr - __uint_as_float(ym & kTop);
+    h = __builtin_amdgcn_perm(yb, xb, kUpper);
+    m = __builtin_amdgcn_perm(ym, xm, kUpper);
+    l = __builtin_amdgcn_perm(__float_as_uint(yl), __float_as_uint(xl), kUpper);
+}
+__device__ __forceinline__ Frag<F32> split_frag(const float (&x)[8]) {
+    Frag<F32> f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[j], y[j], c, 0, 0, 0);
-    return c;
+    for (int j = 0; j < 4; ++j) {
+        uint32_t h, m, l;
+        split3(x[2 * j], x[2 * j + 1], h, m, l);
+        f.p[0][j] = h;
+        f.p[1][j] = m;
+        f.p[2][j] = l;
+    }
+    return f;
+}
+// An infinity becomes the largest finite bfloat16 of its sign.
+__device__ __forceinline__ float finite(float x) {
+    return fabsf(x) == INFINITY ? copysignf(0x1.FEp127f, x) : x;
 }
 
 // Rounds to nearest even, two values to a dword.
@@ -136,7 +179,7 @@ __device__ __forceinline__ void unpack2<F16>(uint32_t w, float &a, float &b) {
     b = static_cast<float>(p[1]);
 }
 
-// The 16 bytes of a fragment or chunk as floats.
+// 16 bytes as floats.
 template <class T>
 __device__ __forceinline__ void unpack_chunk(u32x4 w, float (&x)[16 / T::kSize]) {
     if constexpr (T::kSize == 4) {
@@ -149,18 +192,23 @@ __device__ __forceinline__ void unpack_chunk(u32x4 w, float (&x)[16 / T::kSize])
     }
 }
 
-// Contraction block t of an accumulator as the second operand of a product.
+// Contraction block t (16 rows) of an accumulator as the second operand of a product.
 template <class T>
-__device__ __forceinline__ u32x4 pack_frag(const f32x16 &p, int t) {
-    u32x4 w;
-    if constexpr (T::kSize == 4) {
+__device__ __forceinline__ Frag<T> pack_frag(const f32x16 &p, int t) {
+    Frag<T> f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(p[4 * t + j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack2<T>(p[8 * t + 2 * j], p[8 * t + 2 * j + 1]);
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (T::kPlanes == 3) {
+            uint32_t h, m, l;
+            split3(p[8 * t + 2 * j], p[8 * t + 2 * j + 1], h, m, l);
+            f.p[0][j] = h;
+            f.p[1][j] = m;
+            f.p[2][j] = l;
+        } else {
+            f.p[0][j] = pack2<T>(p[8 * t + 2 * j], p[8 * t + 2 * j + 1]);
+        }
     }
-    return w;
+    return f;
 }
 
 // Four consecutive values, rounded, to a 4-element-aligned address.
@@ -189,30 +237,31 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
 
-// A tile of BN rows of up to DP values, row-major in LDS.  Its 16-byte chunks
-// are permuted within each row by an XOR of the chunk index with bits of the
-// row, so that neither the row reads (32 rows, one chunk) nor the transposed
-// reads (4 rows, 4 chunks) of a wavefront fall on the same banks.
+// A tile of BN rows of up to DP values, row-major in LDS (float32: one such
+// plane per part).  Its 16-byte chunks are permuted within each row by an XOR
+// of the chunk index with bits of the row, so that neither the row reads (32
+// rows, one chunk) nor the transposed reads (4 rows, 4 chunks) of a wavefront
+// fall on the same banks.
 template <class T, int DP>
 struct Tile {
     static constexpr int kSize = T::kSize;
-    static constexpr int EPC = 16 / kSize;      // elements per chunk
+    static constexpr int EPC = 8;               // values per chunk
     static constexpr int CH = DP / EPC;         // chunks per row
     static constexpr int FR = CH / 2;           // fragments over a row
-    static constexpr int ROWB = DP * kSize;     // bytes per row
-    static constexpr int BN = kSize == 4 ? 32 : 64;  // rows per tile
+    static constexpr int ROWB = DP * 2;         // bytes per row
+    static constexpr int BN = T::kPlanes == 3 ? 32 : 64;  // rows per tile
     static constexpr int SUB = BN / 32;
-    static constexpr int NB = 32 / (2 * EPC);   // contraction blocks of 32 rows
+    static constexpr int NB = 2;                // contraction blocks of 32 rows
     static constexpr int DT = DP / 32;          // 32-wide column tiles
-    static constexpr int NCH = BN * CH / kAttnThreads;  // chunks per lane when a workgroup stages a tile
-    static constexpr int kBytes = BN * ROWB;
+    static constexpr int kChunks = BN * CH;     // chunks of a plane
+    static constexpr int NCH = (kChunks + kAttnThreads - 1) / kAttnThreads;  // per lane when a workgroup stages a tile
+    static constexpr int kPlane = BN * ROWB;
+    static constexpr int kBytes = T::kPlanes * kPlane;
 
     __device__ static __forceinline__ int swz(int row, int c) {
-        if constexpr (CH % 16 == 0 && kSize == 4)  // rows of whole bank widths (256 bytes); frag_t reads rows 4 apart
-            return c ^ ((row & 4) << 1 | ((row >> 1) & 4) | (row & 3));
-        else if constexpr (CH % 16 == 0)
+        if constexpr (CH % 16 == 0)      // rows of whole bank widths (256 bytes)
             return c ^ ((row & 3) << 2 | ((row >> 2) & 3));
-        else if constexpr (CH % 8 == 0)  // of 128 bytes and odd multiples: the row's lowest bit moves the banks
+        else if constexpr (CH % 8 == 0)  // of 128 bytes: the row's lowest bit moves the banks
             return c ^ ((row & 2) << 1 | ((row >> 1) & 2) | ((row >> 3) & 1));
         else                             // of 64 and 192: its two lowest bits do
             return c ^ ((row >> 2) & 3);
@@ -220,41 +269,76 @@ struct Tile {
     __device__ static __forceinline__ int at(int row, int c) { return row * ROWB + swz(row, c) * 16; }
 
     // Fragment f of row `row`.
-    __device__ static __forceinline__ u32x4 frag(const char *tile, int row, int f, int half) {
-        return *reinterpret_cast<const u32x4 *>(tile + at(row, 2 * f + half));
+    __device__ static __forceinline__ Frag<T> frag(const char *tile, int row, int f, int half) {
+        Frag<T> r;
+#pragma unroll
+        for (int i = 0; i < T::kPlanes; ++i)
+            r.p[i] = *reinterpret_cast<const u32x4 *>(tile + i * kPlane + at(row, 2 * f + half));
+        return r;
     }
     // First operand with the tile's columns d0 .. d0 + 31 as its rows and the
-    // contraction over 2 EPC tile rows from row0 on, in accumulator order.
-    __device__ static __forceinline__ u32x4 frag_t(const char *tile, int row0, int d0, int lane) {
-        if constexpr (kSize == 4) {
-            const int d = d0 + (lane & 31), row = row0 + 4 * (lane >> 5);
-            u32x4 w;
+    // contraction over 16 tile rows from row0 on, in accumulator order.
+    __device__ static __forceinline__ Frag<T> frag_t(const char *tile, int row0, int d0, int lane) {
+        const int i = lane & 15, row = row0 + 4 * (lane >> 5) + (i >> 2);
+        const int d = d0 + 16 * ((lane >> 4) & 1) + (i & 3) * 4;
+        typedef __attribute__((address_space(3))) i16x4 *lds_ptr;
+        Frag<T> r;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = *reinterpret_cast<const uint32_t *>(tile + at(row + j, d >> 2) + (d & 3) * 4);
-            return w;
-        } else {
-            const int i = lane & 15, row = row0 + 4 * (lane >> 5) + (i >> 2);
-            const int d = d0 + 16 * ((lane >> 4) & 1) + (i & 3) * 4;
-            typedef __attribute__((address_space(3))) i16x4 *lds_ptr;
+        for (int n = 0; n < T::kPlanes; ++n) {
             const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_ptr)(tile + at(row, d >> 3) + (d & 4) * 2));
+                (lds_ptr)(tile + n * kPlane + at(row, d >> 3) + (d & 4) * 2));
             const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_ptr)(tile + at(row + 8, d >> 3) + (d & 4) * 2));
+                (lds_ptr)(tile + n * kPlane + at(row + 8, d >> 3) + (d & 4) * 2));
             const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
-            return u32x4{a.x, a.y, b.x, b.y};
+            r.p[n] = u32x4{a.x, a.y, b.x, b.y};
         }
+        return r;
     }
 };
 
-// Chunk c of a row of `dim` values at `row` (elements); zero past dim.
+// Chunk c (8 values) of a row of `dim` values at `row` (elements), as stored; zero past dim.
 template <class T>
-__device__ __forceinline__ u32x4 load_chunk(const void *base, int64_t row, int c, int dim, bool valid) {
-    constexpr int EPC = 16 / T::kSize;
-    u32x4 w = {0u, 0u, 0u, 0u};
-    if (valid && c * EPC < dim)
-        w = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(base) + (row + c * EPC) * T::kSize);
-    return w;
+struct Raw {
+    u32x4 w[T::kSize / 2];
+};
+template <class T>
+__device__ __forceinline__ Raw<T> load_raw(const void *base, int64_t row, int c, int dim, bool valid) {
+    Raw<T> r;
+#pragma unroll
+    for (int i = 0; i < T::kSize / 2; ++i) r.w[i] = u32x4{0u, 0u, 0u, 0u};
+    if (valid && c * 8 < dim) {
+        const u32x4 *p = reinterpret_cast<const u32x4 *>(static_cast<const char *>(base) + (row + c * 8) * T::kSize);
+#pragma unroll
+        for (int i = 0; i < T::kSize / 2; ++i) r.w[i] = p[i];
+    }
+    return r;
+}
+template <class T>
+__device__ __forceinline__ void unpack_raw(const Raw<T> &r, float (&x)[8]) {
+    if constexpr (T::kSize == 4) {
+        const f32v4 a = __builtin_bit_cast(f32v4, r.w[0]), b = __builtin_bit_cast(f32v4, r.w[1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
+    } else {
+        unpack_chunk<T>(r.w[0], x);
+    }
+}
+// SCORE: the values enter scores (queries, keys).
+template <class T, bool SCORE>
+__device__ __forceinline__ Frag<T> make_frag(const Raw<T> &r) {
+    if constexpr (T::kPlanes == 3) {
+        float x[8];
+        unpack_raw<T>(r, x);
+        if constexpr (SCORE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = finite(x[i]);
+        }
+        return split_frag(x);
+    } else {
+        Frag<T> f;
+        f.p[0] = r.w[0];
+        return f;
+    }
 }
 
 // 16 bytes per lane from global memory straight into LDS: lane l's go to
@@ -267,29 +351,37 @@ __device__ __forceinline__ void load_to_lds(const char *global, char *lds) {
 }
 __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
 
-// One workgroup's staging of a tile: each lane brings NCH chunks.  LDS places
-// are in lane order, so the permutation of the chunks is applied to the global
-// address.  Places that are not loaded (rows past the end, keys that are not
-// attended, chunks past the head's size) keep what they held: zero, or a value
-// of an earlier tile of the same sequence, which only meets factors of zero.
-template <class T, int DP>
+// One workgroup's staging of a tile: each lane brings NCH chunks.  start()
+// begins the loads of a tile, finish() ends them, at the end of the work on the
+// tile before it.
+//
+// 16-bit types go straight into LDS.  LDS places are in lane order, so the
+// permutation of the chunks is applied to the global address.  Places that are
+// not loaded (rows past the end, keys that are not attended, chunks past the
+// head's size) keep what they held: zero, or a value of an earlier tile of the
+// same sequence, which only meets factors of zero.  float32 passes through
+// registers and is split on the way; places that are not loaded become zero.
+template <class T, int DP, bool SCORE>
 struct Loader {
     using TL = Tile<T, DP>;
+    static constexpr bool kDirect = T::kPlanes == 1;
+    static_assert(!kDirect || TL::kChunks % kAttnThreads == 0, "every lane has a chunk");
     const char *p[TL::NCH];
-    uint32_t live;  // bit i: chunk i lies within the head
+    Raw<T> held[kDirect ? 1 : TL::NCH];
+    uint32_t live;  // bit i: chunk i lies within the head (and the tile)
     bool whole;     // every chunk does
 
     __device__ static __forceinline__ int row(int i) { return (static_cast<int>(threadIdx.x) + i * kAttnThreads) / TL::CH; }
     __device__ static __forceinline__ int chunk(int i) {
         const int id = static_cast<int>(threadIdx.x) + i * kAttnThreads;
-        return TL::swz(id / TL::CH, id % TL::CH);
+        return kDirect ? TL::swz(id / TL::CH, id % TL::CH) : id % TL::CH;
     }
     __device__ __forceinline__ void init(int dim) {
         live = 0;
         whole = dim == DP;
 #pragma unroll
         for (int i = 0; i < TL::NCH; ++i)
-            if (chunk(i) * TL::EPC < dim) live |= 1u << i;
+            if (chunk(i) * TL::EPC < dim && static_cast<int>(threadIdx.x) + i * kAttnThreads < TL::kChunks) live |= 1u << i;
     }
     // Rows row0, row0 + 1, ... at `stride` elements.
     __device__ __forceinline__ void point(const void *base, int64_t off, int64_t stride, int64_t row0) {
@@ -304,16 +396,34 @@ struct Loader {
     // Query rows row0, row0 + 1, ... of one key head; those past the last row are not looked at.
     __device__ __forceinline__ void point_rows(const void *base, int64_t off, const HeadStrides &s, int64_t row0,
                                                const AttnArgs &a);
-    // Starts the loads of the rows whose bit of `valid` is set (all: every bit of the tile is).
-    __device__ __forceinline__ void start(char *tile, uint64_t valid, bool all) const {
-        char *at = tile + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * 1024;
-        if (all && whole) {
+    // Begins the loads of the rows whose bit of `valid` is set (all: every bit of the tile is).
+    __device__ __forceinline__ void start(char *tile, uint64_t valid, bool all) {
+        if constexpr (kDirect) {
+            char *at = tile + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * 1024;
+            if (all && whole) {
 #pragma unroll
-            for (int i = 0; i < TL::NCH; ++i) load_to_lds(p[i], at + i * (kAttnThreads * 16));
+                for (int i = 0; i < TL::NCH; ++i) load_to_lds(p[i], at + i * (kAttnThreads * 16));
+            } else {
+#pragma unroll
+                for (int i = 0; i < TL::NCH; ++i)
+                    if (((valid >> row(i)) & (live >> i)) & 1) load_to_lds(p[i], at + i * (kAttnThreads * 16));
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < TL::NCH; ++i)
-                if (((valid >> row(i)) & (live >> i)) & 1) load_to_lds(p[i], at + i * (kAttnThreads * 16));
+                held[i] = load_raw<T>(p[i], 0, 0, 8, ((valid >> (row(i) & 63)) & (live >> i)) & 1);
+        }
+    }
+    __device__ __forceinline__ void finish(char *tile) const {
+        if constexpr (!kDirect) {
+#pragma unroll
+            for (int i = 0; i < TL::NCH; ++i) {
+                if (TL::kChunks % kAttnThreads != 0 && static_cast<int>(threadIdx.x) + i * kAttnThreads >= TL::kChunks) continue;
+                const Frag<T> f = make_frag<T, SCORE>(held[i]);
+#pragma unroll
+                for (int n = 0; n < T::kPlanes; ++n)
+                    *reinterpret_cast<u32x4 *>(tile + n * TL::kPlane + TL::at(row(i), chunk(i))) = f.p[n];
+            }
         }
     }
 };
@@ -364,8 +474,8 @@ __device__ __forceinline__ int64_t row_offset(uint32_t row, const AttnArgs &a, c
     const uint32_t m = div_by(t, a.len_q), i = t - m * a.len_q.d;
     return static_cast<int64_t>(m) * s.b + static_cast<int64_t>(i) * s.t + static_cast<int64_t>(hr) * s.h;
 }
-template <class T, int DP>
-__device__ __forceinline__ void Loader<T, DP>::point_rows(const void *base, int64_t off, const HeadStrides &s,
+template <class T, int DP, bool SCORE>
+__device__ __forceinline__ void Loader<T, DP, SCORE>::point_rows(const void *base, int64_t off, const HeadStrides &s,
                                                           int64_t row0, const AttnArgs &a) {
 #pragma unroll
     for (int i = 0; i < TL::NCH; ++i)

@@ -25,7 +25,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
 
     const uint32_t row0 = (rt * kAttnWaves + wave) * (NR * 32) + col;  // and row0 + 32
     const bool idle = row0 - col >= a.rows;                            // no row of this wavefront exists
-    u32x4 qf[NR][TL::FR], gf[NR][TL::FR];
+    Frag<T> qf[NR][TL::FR], gf[NR][TL::FR];
     f32x16 dq[NR][TL::DT];
     float delta[NR], lse2[NR];
 #pragma unroll
@@ -39,11 +39,12 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
         lse2[n] = INFINITY;  // rows past the end: P = 0
 #pragma unroll
         for (int f = 0; f < TL::FR; ++f) {
-            qf[n][f] = load_chunk<T>(a.q, offq, 2 * f + half, a.D, ok);
-            gf[n][f] = load_chunk<T>(a.dout, offg, 2 * f + half, a.D, ok);
+            qf[n][f] = make_frag<T, true>(load_raw<T>(a.q, offq, 2 * f + half, a.D, ok));
+            const Raw<T> raw = load_raw<T>(a.dout, offg, 2 * f + half, a.D, ok);
+            gf[n][f] = make_frag<T, false>(raw);
             float g[TL::EPC], o[TL::EPC];
-            unpack_chunk<T>(gf[n][f], g);
-            unpack_chunk<T>(load_chunk<T>(a.o_in, offo, 2 * f + half, a.D, ok), o);
+            unpack_raw<T>(raw, g);
+            unpack_raw<T>(load_raw<T>(a.o_in, offo, 2 * f + half, a.D, ok), o);
 #pragma unroll
             for (int i = 0; i < TL::EPC; ++i) delta[n] = fmaf(g[i], o[i], delta[n]);
         }
@@ -63,11 +64,12 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
     const int64_t koff = static_cast<int64_t>(r) * a.sk.b + static_cast<int64_t>(j) * a.sk.h;
     const int64_t voff = static_cast<int64_t>(r) * a.sv.b + static_cast<int64_t>(j) * a.sv.h;
 
-    constexpr uint64_t kAll = TL::BN == 64 ? ~0ull : 0xFFFFFFFFull;
-    Loader<T, DP> gk, gv;
+    constexpr uint64_t kAll = ~0ull >> (64 - TL::BN);
+    Loader<T, DP, true> gk;
+    Loader<T, DP, false> gv;
     uint64_t valid = 0;
     if (first < end) {
-        if (a.D < DP || a.key_mask || (end - first) % TL::BN != 0) {
+        if (T::kPlanes == 1 && (a.D < DP || a.key_mask || (end - first) % TL::BN != 0)) {
             zero_lds<4 * TL::kBytes>(s_kv[0]);
             __syncthreads();
         }
@@ -78,6 +80,8 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
         valid = valid_keys<TL::BN>(r, first, end, a);
         gk.start(s_kv[0], valid, valid == kAll);
         gv.start(s_kv[0] + TL::kBytes, valid, valid == kAll);
+        gk.finish(s_kv[0]);
+        gv.finish(s_kv[0] + TL::kBytes);
     }
     const int64_t kstep = a.sk.t * (TL::BN * T::kSize), vstep = a.sv.t * (TL::BN * T::kSize);
     int buf = 0;
@@ -99,7 +103,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
         for (int t = 0; t < TL::SUB; ++t) {
             const uint32_t live = static_cast<uint32_t>(here >> (32 * t));
             if (live == 0) continue;
-            __builtin_amdgcn_iglp_opt(0);
+            if constexpr (T::kPlanes == 1 && DP <= 64) __builtin_amdgcn_iglp_opt(0);
             f32x16 s[NR], g[NR];
 #pragma unroll
             for (int n = 0; n < NR; ++n)
@@ -107,7 +111,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
                 for (int i = 0; i < 16; ++i) s[n][i] = g[n][i] = 0.f;
 #pragma unroll
             for (int f = 0; f < TL::FR; ++f) {
-                const u32x4 kf = TL::frag(s_k, t * 32 + col, f, half), vf = TL::frag(s_v, t * 32 + col, f, half);
+                const Frag<T> kf = TL::frag(s_k, t * 32 + col, f, half), vf = TL::frag(s_v, t * 32 + col, f, half);
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
                     s[n] = mma<T>(kf, qf[n][f], s[n]);
@@ -129,16 +133,20 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
             }
 #pragma unroll
             for (int b = 0; b < TL::NB; ++b) {
-                u32x4 p[NR];
+                Frag<T> p[NR];
 #pragma unroll
                 for (int n = 0; n < NR; ++n) p[n] = pack_frag<T>(s[n], b);
 #pragma unroll
                 for (int d = 0; d < TL::DT; ++d) {
-                    const u32x4 kf = TL::frag_t(s_k, t * 32 + b * 2 * TL::EPC, d * 32, lane);
+                    const Frag<T> kf = TL::frag_t(s_k, t * 32 + b * 2 * TL::EPC, d * 32, lane);
 #pragma unroll
                     for (int n = 0; n < NR; ++n) dq[n][d] = mma<T>(kf, p[n], dq[n][d]);
                 }
             }
+        }
+        if (key0 + TL::BN < end) {
+            gk.finish(s_kv[buf ^ 1]);
+            gv.finish(s_kv[buf ^ 1] + TL::kBytes);
         }
     }
 #pragma unroll
@@ -181,14 +189,14 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
     bool key_ok = key < n_keys;
     if (a.key_mask && key_ok) key_ok = a.key_mask[static_cast<int64_t>(r) * a.Lk + key] != 0;
     const bool idle = !__any(key_ok);  // no key of this wavefront is attended
-    u32x4 kf[TL::FR], vf[TL::FR];
+    Frag<T> kf[TL::FR], vf[TL::FR];
     {
         const int64_t offk = static_cast<int64_t>(r) * a.sk.b + static_cast<int64_t>(j) * a.sk.h + (key_ok ? key * a.sk.t : 0);
         const int64_t offv = static_cast<int64_t>(r) * a.sv.b + static_cast<int64_t>(j) * a.sv.h + (key_ok ? key * a.sv.t : 0);
 #pragma unroll
         for (int f = 0; f < TL::FR; ++f) {
-            kf[f] = load_chunk<T>(a.k, offk, 2 * f + half, a.D, key_ok);
-            vf[f] = load_chunk<T>(a.v, offv, 2 * f + half, a.D, key_ok);
+            kf[f] = make_frag<T, true>(load_raw<T>(a.k, offk, 2 * f + half, a.D, key_ok));
+            vf[f] = make_frag<T, false>(load_raw<T>(a.v, offv, 2 * f + half, a.D, key_ok));
         }
     }
     f32x16 dk[TL::DT], dv[TL::DT];
@@ -203,8 +211,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
     const int64_t baseq = pair_offset(r, j, a, a.sq), baseg = pair_offset(r, j, a, a.sdo);
     const float *delta = a.delta + static_cast<int64_t>(pair) * a.rows;
 
-    constexpr uint64_t kAll = TL::BN == 64 ? ~0ull : 0xFFFFFFFFull;
-    Loader<T, DP> gq, gg;
+    constexpr uint64_t kAll = ~0ull >> (64 - TL::BN);
+    Loader<T, DP, true> gq;
+    Loader<T, DP, false> gg;
     float g_lse = 0.f, g_delta = 0.f;
     // With whole groups of rep rows in a tile and the maps in one run, a tile's
     // rows lie a constant step after the last tile's.
@@ -234,7 +243,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
         }
     };
     if (first < end) {
-        if (a.D < DP || (end - first) % TL::BN != 0) {
+        if (T::kPlanes == 1 && (a.D < DP || (end - first) % TL::BN != 0)) {
             zero_lds<4 * TL::kBytes>(s_qg[0]);
             __syncthreads();
         }
@@ -242,6 +251,8 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
         gg.init(a.D);
         point(first);
         start(first, 0);
+        gq.finish(s_qg[0]);
+        gg.finish(s_qg[0] + TL::kBytes);
     }
     int buf = 0;
     for (int64_t row0 = first; row0 < end; row0 += TL::BN, buf ^= 1) {
@@ -260,11 +271,11 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
             }
             start(row0 + TL::BN, buf ^ 1);
         }
-        if (idle) continue;
 #pragma unroll
         for (int t = 0; t < TL::SUB; ++t) {
+            if (idle) break;
             // Reads of LDS spread between the products: 679 -> 651 us for the 2048-map training batch (forward included).
-            __builtin_amdgcn_iglp_opt(0);
+            if constexpr (T::kPlanes == 1 && DP <= 64) __builtin_amdgcn_iglp_opt(0);
             f32x16 s, g;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = 0.f;
@@ -290,13 +301,17 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
             }
 #pragma unroll
             for (int b = 0; b < TL::NB; ++b) {
-                const u32x4 p = pack_frag<T>(s, b), ds = pack_frag<T>(g, b);
+                const Frag<T> p = pack_frag<T>(s, b), ds = pack_frag<T>(g, b);
 #pragma unroll
                 for (int d = 0; d < TL::DT; ++d) {
                     dv[d] = mma<T>(TL::frag_t(s_g, t * 32 + b * 2 * TL::EPC, d * 32, lane), p, dv[d]);
                     dk[d] = mma<T>(TL::frag_t(s_q, t * 32 + b * 2 * TL::EPC, d * 32, lane), ds, dk[d]);
                 }
             }
+        }
+        if (row0 + TL::BN < end) {
+            gq.finish(s_qg[buf ^ 1]);
+            gg.finish(s_qg[buf ^ 1] + TL::kBytes);
         }
     }
     const bool in = key < a.Lk;

@@ -34,7 +34,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
 
     const uint32_t row0 = (rt * kAttnWaves + wave) * (NR * 32) + col;  // and row0 + 32
     const bool idle = row0 - col >= a.rows;                            // no row of this wavefront exists
-    u32x4 qf[NR][TL::FR];
+    Frag<T> qf[NR][TL::FR];
     f32x16 o[NR][TL::DT];
     float m[NR], l[NR];
 #pragma unroll
@@ -43,7 +43,8 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
         const bool ok = row < a.rows;
         const int64_t off = pair_offset(r, j, a, a.sq) + (ok ? row_offset(row, a, a.sq) : 0);
 #pragma unroll
-        for (int f = 0; f < TL::FR; ++f) qf[n][f] = load_chunk<T>(a.q, off, 2 * f + half, a.D, ok);
+        for (int f = 0; f < TL::FR; ++f) 
+            qf[n][f] = make_frag<T, true>(load_raw<T>(a.q, off, 2 * f + half, a.D, ok));
 #pragma unroll
         for (int d = 0; d < TL::DT; ++d)
 #pragma unroll
@@ -59,12 +60,13 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
     const int64_t koff = static_cast<int64_t>(r) * a.sk.b + static_cast<int64_t>(j) * a.sk.h;
     const int64_t voff = static_cast<int64_t>(r) * a.sv.b + static_cast<int64_t>(j) * a.sv.h;
 
-    constexpr uint64_t kAll = TL::BN == 64 ? ~0ull : 0xFFFFFFFFull;
-    Loader<T, DP> gk, gv;
+    constexpr uint64_t kAll = ~0ull >> (64 - TL::BN);
+    Loader<T, DP, true> gk;
+    Loader<T, DP, false> gv;
     uint64_t valid = 0;
     bool seen = false;
     if (first < end) {
-        if (a.D < DP || a.key_mask || (end - first) % TL::BN != 0) {
+        if (T::kPlanes == 1 && (a.D < DP || a.key_mask || (end - first) % TL::BN != 0)) {
             zero_lds<4 * TL::kBytes>(s_kv[0]);
             __syncthreads();
         }
@@ -75,6 +77,8 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
         valid = valid_keys<TL::BN>(r, first, end, a);
         gk.start(s_kv[0], valid, valid == kAll);
         gv.start(s_kv[0] + TL::kBytes, valid, valid == kAll);
+        gk.finish(s_kv[0]);
+        gv.finish(s_kv[0] + TL::kBytes);
     }
     const int64_t kstep = a.sk.t * (TL::BN * T::kSize), vstep = a.sv.t * (TL::BN * T::kSize);
     int buf = 0;
@@ -100,7 +104,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
                     for (int i = 0; i < 16; ++i) s[n][t][i] = 0.f;
 #pragma unroll
                 for (int f = 0; f < TL::FR; ++f) {
-                    const u32x4 kf = TL::frag(s_k, t * 32 + col, f, half);
+                    const Frag<T> kf = TL::frag(s_k, t * 32 + col, f, half);
 #pragma unroll
                     for (int n = 0; n < NR; ++n) s[n][t] = mma<T>(kf, qf[n][f], s[n][t]);
                 }
@@ -162,16 +166,20 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
             for (int t = 0; t < TL::SUB; ++t)
 #pragma unroll
                 for (int b = 0; b < TL::NB; ++b) {
-                    u32x4 p[NR];
+                    Frag<T> p[NR];
 #pragma unroll
                     for (int n = 0; n < NR; ++n) p[n] = pack_frag<T>(s[n][t], b);
 #pragma unroll
                     for (int d = 0; d < TL::DT; ++d) {
-                        const u32x4 vf = TL::frag_t(s_v, t * 32 + b * 2 * TL::EPC, d * 32, lane);
+                        const Frag<T> vf = TL::frag_t(s_v, t * 32 + b * 2 * TL::EPC, d * 32, lane);
 #pragma unroll
                         for (int n = 0; n < NR; ++n) o[n][d] = mma<T>(vf, p[n], o[n][d]);
                     }
                 }
+        }
+        if (key0 + TL::BN < end) {
+            gk.finish(s_kv[buf ^ 1]);
+            gv.finish(s_kv[buf ^ 1] + TL::kBytes);
         }
         valid = next;
     }
