@@ -1,0 +1,174 @@
+"""A small conditional denoiser made of the library's attention operators, trained a little and sampled.
+
+The 64 beads of a map are its tokens (a token's features are its row of distances); the region's conditioning is a
+sequence of encoder states of another length.  Queries and keys are normalised per head and rotated by their bead's
+position on the chain, the tokens attend to the states of their region, and a projection gives the noise prediction
+of the map.  All maps of a region (guidance weights x trajectories) share its keys and values.
+
+    python examples/attention_denoiser.py --train 30 --steps 10
+
+Random weights and synthetic conditioning: it shows the calls, not a model.
+"""
+
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+
+import numpy as np
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+if ROOT not in sys.path:
+    sys.path.insert(0, ROOT)
+
+import tiled_genome_diffusion_amd as pc  # noqa: E402
+from workloads import Workload, reference_maps  # noqa: E402
+
+BEADS = pc.BEADS
+
+
+class CrossAttention(torch.autograd.Function):
+    """pc_cross_attention with its gradients."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, kv_len):
+        out = torch.empty_like(q)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        pc.pc_cross_attention(q, k, v, out, lse, kv_len)
+        ctx.save_for_backward(q, k, v, out, lse, kv_len)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, out, lse, kv_len = ctx.saved_tensors
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        pc.pc_cross_attention_backward(q, k, v, out, lse, dout.contiguous(), dq, dk, dv, kv_len)
+        return dq, dk, dv, None
+
+
+class QKNormRope(torch.autograd.Function):
+    """pc_qk_norm_rope with its gradients."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, pos_q, pos_k, freqs):
+        q_out, k_out = torch.empty_like(q), torch.empty_like(k)
+        pc.pc_qk_norm_rope(q, k, wq, wk, pos_q, pos_k, freqs, q_out, k_out)
+        ctx.save_for_backward(q, k, wq, wk, pos_q, pos_k)
+        ctx.freqs = freqs
+        return q_out, k_out
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, wq, wk, pos_q, pos_k = ctx.saved_tensors
+        dq, dk, dwq, dwk = (torch.empty_like(t) for t in (q, k, wq, wk))
+        pc.pc_qk_norm_rope_backward(q, k, wq, wk, pos_q, pos_k, ctx.freqs, dq_out.contiguous(), dk_out.contiguous(), dq,
+                                    dk, dwq, dwk)
+        return dq, dk, dwq, dwk, None, None, None
+
+
+class Denoiser(torch.nn.Module):
+    """eps(x, states): packed maps [n_maps, 2016] -> packed noise predictions."""
+
+    def __init__(self, width: int, heads: int = 4, heads_kv: int = 2, dim: int = 32, seed: int = 0):
+        super().__init__()
+        gen = torch.Generator().manual_seed(seed)
+
+        def weight(*s):
+            return torch.nn.Parameter(torch.randn(*s, generator=gen) / s[0] ** 0.5)
+
+        self.heads, self.heads_kv, self.dim = heads, heads_kv, dim
+        self.wq, self.wkv = weight(BEADS, heads * dim), weight(width, 2 * heads_kv * dim)
+        self.wo, self.skip = weight(heads * dim, BEADS), weight(BEADS, BEADS)
+        self.nq, self.nk = torch.nn.Parameter(torch.ones(dim)), torch.nn.Parameter(torch.ones(dim))
+        self.freqs = 1000.0 ** (-np.arange(0, dim, 2, dtype=np.float64) / dim)
+        i, j = torch.triu_indices(BEADS, BEADS, offset=1).unbind()
+        self.register_buffer("row", i)
+        self.register_buffer("col", j)
+
+    def forward(self, x, states, kv_len, pos_q, pos_k):
+        B, (R, L, _) = x.shape[0], states.shape
+        full = x.new_zeros(B, BEADS, BEADS)
+        full[:, self.row, self.col] = x
+        full = full + full.transpose(1, 2)
+        q = torch.matmul(full.view(B * BEADS, BEADS), self.wq).view(B, BEADS, self.heads, self.dim)
+        kv = torch.matmul(states.reshape(R * L, -1), self.wkv).view(R, L, 2, self.heads_kv, self.dim)
+        q, k = QKNormRope.apply(q, kv[:, :, 0], self.nq, self.nk, pos_q, pos_k, self.freqs)
+        a = CrossAttention.apply(q, k, kv[:, :, 1], kv_len)
+        y = torch.matmul(a.reshape(B * BEADS, -1), self.wo) + torch.matmul(full.view(B * BEADS, BEADS), self.skip)
+        y = y.view(B, BEADS, BEADS)
+        return 0.5 * (y + y.transpose(1, 2))[:, self.row, self.col]
+
+
+def setup(wl: Workload, len_k: int, width: int, seed: int, device):
+    """Conditional and null states, their lengths, and the positions of beads and bins on the chain."""
+    gen = torch.Generator().manual_seed(seed)
+    R, group = wl.n_regions, wl.n_guidance * wl.n_traj
+    states = torch.randn(R, len_k, width, generator=gen).to(device)
+    null = torch.zeros_like(states)
+    kv_len = torch.randint(len_k // 2, len_k + 1, (R,), generator=gen, dtype=torch.int32).to(device)
+    start = torch.arange(R, dtype=torch.int32) % max(wl.chain_len, 1) * wl.stride
+    pos_q = (start.repeat_interleave(group)[:, None] + torch.arange(BEADS, dtype=torch.int32)).to(device)
+    pos_k = (start[:, None] + torch.arange(len_k, dtype=torch.int32)).to(device)
+    return states, null, kv_len, pos_q, pos_k
+
+
+def train(model, wl: Workload, inputs, steps: int, seed: int, lr: float = 3e-3):
+    """Noise prediction at random steps of the schedule for the regions' reference maps; returns the losses."""
+    states, _, kv_len, pos_q, pos_k = inputs
+    x0 = torch.from_numpy(reference_maps(wl, seed)[0]).to(states.device)
+    x0 = x0.repeat_interleave(wl.n_guidance * wl.n_traj, dim=0)
+    abar = torch.from_numpy(pc.pc_ddim_schedule(50)[0].astype(np.float32)).to(states.device)
+    gen = torch.Generator(device=states.device).manual_seed(seed)
+    opt = torch.optim.Adam(model.parameters(), lr=lr)
+    losses = []
+    for _ in range(steps):
+        a = abar[torch.randint(0, 50, (x0.shape[0], 1), generator=gen, device=x0.device)]
+        eps = torch.randn(x0.shape, generator=gen, device=x0.device)
+        loss = (model(a.sqrt() * x0 + (1 - a).sqrt() * eps, states, kv_len, pos_q, pos_k) - eps).square().mean()
+        opt.zero_grad()
+        loss.backward()
+        opt.step()
+        losses.append(float(loss.detach()))
+    return losses
+
+
+@torch.no_grad()
+def sample(model, wl: Workload, inputs, n_steps: int, seed: int):
+    """The guided reverse chain with the network's predictions, seams projected after every step; packed final maps."""
+    states, null, kv_len, pos_q, pos_k = inputs
+    lay = pc.PCLayout(wl.n_regions, wl.n_guidance, wl.n_traj, wl.chain_len, wl.overlap if wl.chain_len > 1 else 0)
+    x = torch.empty(lay.n_maps, pc.PACKED, device=states.device)
+    pc.pc_init_state(x, lay, seed)
+    a_t, a_n = pc.pc_ddim_schedule(n_steps)
+    for i in range(n_steps):
+        eps_c = model(x, states, kv_len, pos_q, pos_k).contiguous()
+        eps_u = model(x, null, kv_len, pos_q, pos_k).contiguous()
+        pc.pc_ddim_cfg_step_eps(x, eps_c, eps_u, list(wl.w), lay, a_t[i], a_n[i], wl.eta, seed, i + 1,
+                                project_seams=wl.chain_len > 1)
+    return x
+
+
+def main():
+    p = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
+    p.add_argument("--train", type=int, default=30, help="training steps")
+    p.add_argument("--steps", type=int, default=10, help="DDIM steps")
+    p.add_argument("--seed", type=int, default=0)
+    a = p.parse_args()
+    dev = torch.device("cuda:0")
+    wl = Workload("small_chain", "", 4, 2, 8, 4, 12, 52, (a.steps,), 1.0, (0.0, 1.0), None, 3)
+    inputs = setup(wl, 150, 96, a.seed, dev)
+    model = Denoiser(96).to(dev)
+    losses = train(model, wl, inputs, a.train, a.seed)
+    if losses:
+        print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f} in {len(losses)} steps", flush=True)
+    x = sample(model, wl, inputs, a.steps, a.seed)
+    coords = torch.empty(x.shape[0] * BEADS * 3, device=dev)
+    pc.pc_mds_recover(x, coords)
+    print(f"{x.shape[0]} maps, mean distance {float(x.mean()):.3f}, coordinates finite: "
+          f"{bool(torch.isfinite(coords).all())}", flush=True)
+
+
+if __name__ == "__main__":
+    main()
