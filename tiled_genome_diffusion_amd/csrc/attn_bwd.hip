@@ -337,29 +337,43 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
     }
 }
 
-// Adds the splits' partial sums [split][pair][n][D] in split order and rounds
-// once.  ROWS: the query rows of dq; otherwise the keys of dk or dv.
-template <bool ROWS>
-__global__ __launch_bounds__(256) void k_attn_sum(const AttnArgs a, const float *part, void *out, HeadStrides so,
-                                                  int32_t dtype, int64_t total, int64_t block0) {
-    const int64_t id = (block0 + blockIdx.x) * 256 + threadIdx.x;
-    if (id >= total) return;
-    const uint32_t n = ROWS ? a.rows : static_cast<uint32_t>(a.Lk), quads = a.D / 4;
+// One gradient whose splits are to be added: partial sums [split][pair][n][D].
+struct SumJob {
+    const float *part;
+    void *out;
+    HeadStrides so;
+    int64_t total;     // quads of the output; 0: nothing to do
+    uint32_t n;        // query rows or keys of a pair
+    uint32_t n_split;
+    bool rows;         // query rows
+};
+struct SumJobs {
+    SumJob job[3];
+};
+
+// Adds the partial sums of up to three gradients in split order and rounds once.
+__global__ __launch_bounds__(256) void k_attn_sum(const AttnArgs a, const SumJobs jobs, int32_t dtype, int64_t block0) {
+    int64_t id = (block0 + blockIdx.x) * 256 + threadIdx.x;
+    int k = 0;
+    while (k < 3 && id >= jobs.job[k].total) id -= jobs.job[k++].total;
+    if (k == 3) return;
+    const SumJob &g = jobs.job[k];
+    const uint32_t quads = a.D / 4;
     const int64_t slot = id / quads;
     const int d = static_cast<int>(id - slot * quads) * 4;
-    const uint32_t pair = static_cast<uint32_t>(slot / n), at = static_cast<uint32_t>(slot - static_cast<int64_t>(pair) * n);
+    const uint32_t pair = static_cast<uint32_t>(slot / g.n), at = static_cast<uint32_t>(slot - static_cast<int64_t>(pair) * g.n);
     const uint32_t r = pair / a.Hk, j = pair - r * a.Hk;
     f32v4 x = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t s = 0; s < a.n_split.d; ++s)
-        x += *reinterpret_cast<const f32v4 *>(part + (static_cast<int64_t>(s) * a.n_kv * a.Hk * n + slot) * a.D + d);
-    const int64_t off = d + (ROWS ? pair_offset(r, j, a, so) + row_offset(at, a, so)
-                                  : static_cast<int64_t>(r) * so.b + static_cast<int64_t>(j) * so.h + at * so.t);
+    for (uint32_t s = 0; s < g.n_split; ++s)
+        x += *reinterpret_cast<const f32v4 *>(g.part + (static_cast<int64_t>(s) * a.n_kv * a.Hk * g.n + slot) * a.D + d);
+    const int64_t off = d + (g.rows ? pair_offset(r, j, a, g.so) + row_offset(at, a, g.so)
+                                    : static_cast<int64_t>(r) * g.so.b + static_cast<int64_t>(j) * g.so.h + at * g.so.t);
     if (dtype == kBf16)
-        store4<Bf16>(out, off, x[0], x[1], x[2], x[3]);
+        store4<Bf16>(g.out, off, x[0], x[1], x[2], x[3]);
     else if (dtype == kF16)
-        store4<F16>(out, off, x[0], x[1], x[2], x[3]);
+        store4<F16>(g.out, off, x[0], x[1], x[2], x[3]);
     else
-        store4<F32>(out, off, x[0], x[1], x[2], x[3]);
+        store4<F32>(g.out, off, x[0], x[1], x[2], x[3]);
 }
 
 struct BwdPlan {
@@ -372,42 +386,32 @@ BwdPlan bwd_plan(const AttnArgs &a, int32_t dtype) {
     BwdPlan p;
     p.pairs = static_cast<int64_t>(a.n_kv) * a.Hk;
     p.nr = attn_row_blocks(a, dtype);
-    p.q = attn_plan(p.pairs, (static_cast<int64_t>(a.rows) + 128 * p.nr - 1) / (128 * p.nr), (a.Lk + bn - 1) / bn, 4);
-    p.kv = attn_plan(p.pairs, (static_cast<int64_t>(a.Lk) + 127) / 128, (a.rows + bn - 1) / bn, 4);
+    p.q = attn_plan(p.pairs, (static_cast<int64_t>(a.rows) + 128 * p.nr - 1) / (128 * p.nr), (a.Lk + bn - 1) / bn, kSplitLeast / bn);
+    p.kv = attn_plan(p.pairs, (static_cast<int64_t>(a.Lk) + 127) / 128, (a.rows + bn - 1) / bn, kSplitLeast / bn);
     p.bytes_delta = round16(p.pairs * a.rows * 4);
     p.bytes_q = p.q.n_split > 1 ? p.q.n_split * p.pairs * a.rows * a.D * 4 : 0;
     p.bytes_kv = p.kv.n_split > 1 ? 2 * p.kv.n_split * p.pairs * a.Lk * a.D * 4 : 0;
     return p;
 }
 
-template <bool ROWS>
-hipError_t sum_splits(const AttnArgs &a, const float *part, void *out, const HeadStrides &so, int32_t dtype, int64_t n,
-                      hipStream_t stream) {
-    const int64_t total = static_cast<int64_t>(a.n_kv) * a.Hk * n * (a.D / 4);
-    return launch_slices((total + 255) / 256, 256, [&](int64_t first, uint32_t count) {
-        k_attn_sum<ROWS><<<count, 256, 0, stream>>>(a, part, out, so, dtype, total, first);
-    });
-}
-
 }  // namespace
 
-// delta, then the partial sums of dq, which those of dk and dv follow in time
-// and may overwrite.
+// delta, the partial sums of dq, those of dk and dv.
 int64_t attn_bwd_workspace(const AttnArgs &a, int32_t dtype) {
     const BwdPlan p = bwd_plan(a, dtype);
-    return p.bytes_delta + (p.bytes_q > p.bytes_kv ? p.bytes_q : p.bytes_kv);
+    return p.bytes_delta + p.bytes_q + p.bytes_kv;
 }
 
 hipError_t launch_attn_bwd(AttnArgs a, int32_t dtype, char *workspace, hipStream_t stream) {
     const BwdPlan p = bwd_plan(a, dtype);
     a.delta = reinterpret_cast<float *>(workspace);
-    a.part = reinterpret_cast<float *>(workspace + p.bytes_delta);
-    hipError_t e = hipSuccess;
-    a.n_tiles = fast_div(static_cast<uint32_t>(p.q.n_tiles));
-    a.n_split = fast_div(static_cast<uint32_t>(p.q.n_split));
-    a.split_tiles = static_cast<uint32_t>(p.q.split_tiles);
+    SumJobs jobs{};
     if (a.rows > 0) {
-        e = launch_slices(p.pairs * p.q.n_split * p.q.n_tiles, kAttnThreads, [&](int64_t first, uint32_t count) {
+        a.part = reinterpret_cast<float *>(workspace + p.bytes_delta);
+        a.n_tiles = fast_div(static_cast<uint32_t>(p.q.n_tiles));
+        a.n_split = fast_div(static_cast<uint32_t>(p.q.n_split));
+        a.split_tiles = static_cast<uint32_t>(p.q.split_tiles);
+        const hipError_t e = launch_slices(p.pairs * p.q.n_split * p.q.n_tiles, kAttnThreads, [&](int64_t first, uint32_t count) {
             for_dtype_dim(dtype, a.D, [&](auto type, auto dim) {
                 using T = decltype(type);
                 constexpr int DP = decltype(dim)::value;
@@ -420,26 +424,38 @@ hipError_t launch_attn_bwd(AttnArgs a, int32_t dtype, char *workspace, hipStream
                     k_attn_dq<T, DP, 1, false><<<count, kAttnThreads, 0, stream>>>(a, first);
             });
         });
-        if (e == hipSuccess && p.q.n_split > 1) e = sum_splits<true>(a, a.part, a.dq, a.sdq, dtype, a.rows, stream);
+        if (e != hipSuccess) return e;
+        if (p.q.n_split > 1)
+            jobs.job[0] = SumJob{a.part, a.dq, a.sdq, p.pairs * a.rows * (a.D / 4), a.rows,
+                                 static_cast<uint32_t>(p.q.n_split), true};
     }
-    if (e != hipSuccess || a.Lk == 0) return e;
-    a.n_tiles = fast_div(static_cast<uint32_t>(p.kv.n_tiles));
-    a.n_split = fast_div(static_cast<uint32_t>(p.kv.n_split));
-    a.split_tiles = static_cast<uint32_t>(p.kv.split_tiles);
-    e = launch_slices(p.pairs * p.kv.n_split * p.kv.n_tiles, kAttnThreads, [&](int64_t first, uint32_t count) {
-        for_dtype_dim(dtype, a.D, [&](auto type, auto dim) {
-            using T = decltype(type);
-            constexpr int DP = decltype(dim)::value;
-            if (p.kv.n_split > 1)
-                k_attn_dkv<T, DP, true><<<count, kAttnThreads, 0, stream>>>(a, first);
-            else
-                k_attn_dkv<T, DP, false><<<count, kAttnThreads, 0, stream>>>(a, first);
+    if (a.Lk > 0) {
+        a.part = reinterpret_cast<float *>(workspace + p.bytes_delta + p.bytes_q);
+        a.n_tiles = fast_div(static_cast<uint32_t>(p.kv.n_tiles));
+        a.n_split = fast_div(static_cast<uint32_t>(p.kv.n_split));
+        a.split_tiles = static_cast<uint32_t>(p.kv.split_tiles);
+        const hipError_t e = launch_slices(p.pairs * p.kv.n_split * p.kv.n_tiles, kAttnThreads, [&](int64_t first, uint32_t count) {
+            for_dtype_dim(dtype, a.D, [&](auto type, auto dim) {
+                using T = decltype(type);
+                constexpr int DP = decltype(dim)::value;
+                if (p.kv.n_split > 1)
+                    k_attn_dkv<T, DP, true><<<count, kAttnThreads, 0, stream>>>(a, first);
+                else
+                    k_attn_dkv<T, DP, false><<<count, kAttnThreads, 0, stream>>>(a, first);
+            });
         });
+        if (e != hipSuccess) return e;
+        if (p.kv.n_split > 1) {
+            const int64_t total = p.pairs * a.Lk * (a.D / 4);
+            const uint32_t n = static_cast<uint32_t>(a.Lk), s = static_cast<uint32_t>(p.kv.n_split);
+            jobs.job[1] = SumJob{a.part, a.dk, a.sdk, total, n, s, false};
+            jobs.job[2] = SumJob{a.part + p.kv.n_split * p.pairs * a.Lk * a.D, a.dv, a.sdv, total, n, s, false};
+        }
+    }
+    const int64_t quads = jobs.job[0].total + jobs.job[1].total + jobs.job[2].total;
+    return launch_slices((quads + 255) / 256, 256, [&](int64_t first, uint32_t count) {
+        k_attn_sum<<<count, 256, 0, stream>>>(a, jobs, dtype, first);
     });
-    if (e != hipSuccess || p.kv.n_split == 1) return e;
-    const float *part_v = a.part + p.kv.n_split * p.pairs * a.Lk * a.D;
-    e = sum_splits<false>(a, a.part, a.dk, a.sdk, dtype, a.Lk, stream);
-    return e != hipSuccess ? e : sum_splits<false>(a, part_v, a.dv, a.sdv, dtype, a.Lk, stream);
 }
 
 }  // namespace pc

@@ -264,7 +264,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int32_t dty
 AttnPlan attn_fwd_plan(const AttnArgs &a, int32_t dtype) {
     const int bn = dtype == kF32 ? 32 : 64;
     const int64_t rows = 128 * attn_row_blocks(a, dtype);
-    return attn_plan(static_cast<int64_t>(a.n_kv) * a.Hk, (a.rows + rows - 1) / rows, (a.Lk + bn - 1) / bn, 4);
+    return attn_plan(static_cast<int64_t>(a.n_kv) * a.Hk, (a.rows + rows - 1) / rows, (a.Lk + bn - 1) / bn, kSplitLeast / bn);
 }
 
 int64_t attn_fwd_workspace(const AttnArgs &a, int32_t dtype) {
