@@ -63,7 +63,7 @@ struct AttnArgs {
     const uint8_t *key_mask;
     float *part;        // workspace: partial sums of a split (see the kernels)
     float *part_ml;     // forward split: running maximum and sum
-    float *delta;       // backward: rowsum(dout o out) per row
+    float *delta;       // backward: rowsum(P o dP) per row
     HeadStrides sq, sk, sv, so, sdo, sdq, sdk, sdv;
     FastDiv rep, len_q, heads_kv, n_split, n_tiles;
     int32_t n_kv, group, Lq, Lk, H, Hk, D;
