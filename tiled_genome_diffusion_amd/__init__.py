@@ -349,8 +349,14 @@ def pc_cross_attention(q, k, v, out, lse=None, kv_len=None, key_mask=None, scale
     ptrs = (pq, pk, pv, _flat(kv_len, "kv_len", t.int32, kshape[:1], q),
             _flat(_mask(key_mask), "key_mask", t.uint8, kshape[:2], q), po,
             _flat(lse, "lse", t.float32, shape[:3], q))
-    p, size, keep = _workspace(workspace, lambda: _attention_bytes(a, False, "pc_cross_attention"), q)
-    _check(_enqueue(q, _lib.load().pc_cross_attention, a, *ptrs, p, size), "pc_cross_attention")
+    func = _lib.load().pc_cross_attention
+    if workspace is None:   # most calls need none: asked for only where the call is refused without one
+        status = _enqueue(q, func, a, *ptrs, None, 0)
+        if status == 0 or status != -1 or not (need := _attention_bytes(a, False, "pc_cross_attention")):
+            return _check(status, "pc_cross_attention")
+        workspace = t.empty(need, dtype=t.uint8, device=q.device)
+    p, size, keep = _workspace(workspace, None, q)
+    _check(_enqueue(q, func, a, *ptrs, p, size), "pc_cross_attention")
 
 
 def pc_cross_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, kv_len=None, key_mask=None, scale=None,
@@ -405,8 +411,9 @@ def _norm_side(name: str, ref, x, weight=None, positions=None, y=None, dy=None, 
 
 
 def _freqs(freqs):
-    f = np.ascontiguousarray(freqs, dtype=np.float64).reshape(-1)
-    return f, f.ctypes.data if f.size else None
+    """(rotated values, the frequencies' bytes)."""
+    f = np.asarray(freqs, dtype=np.float64)
+    return 2 * f.size, f.tobytes() if f.size else None
 
 
 def _norm_ref(q, k):
@@ -429,8 +436,8 @@ def pc_qk_norm_rope(q, k, q_weight, k_weight, q_positions, k_positions, freqs, q
     dtype = _dtype(ref, "q" if q is not None else "k")
     sq = _norm_side("q", ref, q, q_weight, q_positions, q_out)
     sk = _norm_side("k", ref, k, k_weight, k_positions, k_out)
-    f, fp = _freqs(freqs)
-    _check(_enqueue(ref, _lib.load().pc_qk_norm_rope, sq, sk, dtype, ref.shape[3], 2 * f.size, fp,
+    rot, f = _freqs(freqs)
+    _check(_enqueue(ref, _lib.load().pc_qk_norm_rope, sq, sk, dtype, ref.shape[3], rot, f,
                     1 if interleaved else 0, eps), "pc_qk_norm_rope")
 
 
@@ -456,10 +463,10 @@ def pc_qk_norm_rope_backward(q, k, q_weight, k_weight, q_positions, k_positions,
     dtype = _dtype(ref, "q" if q is not None else "k")
     sq = _norm_side("q", ref, q, q_weight, q_positions, None, dq_out, dq, dq_weight)
     sk = _norm_side("k", ref, k, k_weight, k_positions, None, dk_out, dk, dk_weight)
-    f, fp = _freqs(freqs)
+    rot, f = _freqs(freqs)
     D = ref.shape[3]
-    p, size, keep = _workspace(workspace, lambda: _norm_bytes(sq, sk, dtype, D, 2 * f.size, "pc_qk_norm_rope_backward"), ref)
-    _check(_enqueue(ref, _lib.load().pc_qk_norm_rope_backward, sq, sk, dtype, D, 2 * f.size, fp, 1 if interleaved else 0,
+    p, size, keep = _workspace(workspace, lambda: _norm_bytes(sq, sk, dtype, D, rot, "pc_qk_norm_rope_backward"), ref)
+    _check(_enqueue(ref, _lib.load().pc_qk_norm_rope_backward, sq, sk, dtype, D, rot, f, 1 if interleaved else 0,
                     eps, p, size), "pc_qk_norm_rope_backward")
 
 
