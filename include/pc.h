@@ -339,6 +339,8 @@ PC_API pc_status pc_cross_attention_workspace(const pc_attention *a, int32_t bac
  * places that are not attended (NaN, too) has no influence.
  * Scores, softmax statistics and sums are float32; the probabilities are
  * rounded to the tensors' type for their product with v, the output once.
+ * PC_F32 keeps float32's precision throughout (an infinite value of q or k
+ * counts as the largest bfloat16, one of v gives NaN).
  * The result is deterministic.
  *   q          device [n_kv group][len_q][heads][dim].
  *   k, v       device [n_kv][len_k][heads_kv][dim].
@@ -362,6 +364,8 @@ PC_API pc_status pc_cross_attention(const pc_attention *a, const void *q, const 
  *   dq = scale dS k, dk = scale dS^T q, dv = P^T dout,
  * dk and dv summed over all query batches and heads that read the key head.
  * Places that are not attended get zeros.  Deterministic: no atomic sums.
+ * P and dS are rounded to the tensors' type for their products: with PC_F16
+ * |P (dP - rowsum)| has to stay below 65504.
  *   out, lse      of the forward call (lse is required here).
  *   dout          device, as out.
  *   dq, dk, dv    device, as q, k, v, written.  None may overlap another array of the call.
@@ -376,7 +380,7 @@ PC_API pc_status pc_cross_attention_backward(const pc_attention *a, const void *
  * One side (queries or keys) of pc_qk_norm_rope: [batch][len][heads][dim].
  */
 typedef struct pc_norm_side {
-    int32_t batch, len, heads;   /* batch, len >= 0, heads >= 1                             */
+    int32_t batch, len, heads;   /* batch, len >= 0, heads in 1..2^20                       */
     const void *x;               /* device, read                                            */
     void *y;                     /* device, forward: written; may be x (with x's strides)   */
     const float *weight;         /* device float [dim] or NULL (ones)                       */

@@ -19,6 +19,14 @@ namespace {
 // wavefront takes its maximum as its base and l and O are scaled to it; P
 // stays below 2^kSlack, so neither float32 nor float16 can overflow, and the
 // scaling of O (one instruction per score at dim 64) is rare.
+//
+// Measured (bfloat16, heads of 64, 16,384 maps of 64 tokens and 8 heads over
+// 32 states of 512 keys): 1.40 ms, 789 TFLOP/s, of a library product's 1144.
+// The card's power sets it: the clock is 1.85 to 1.9 GHz, with the vector
+// units 73% and the matrix units 39% busy; forms with fewer instructions ran
+// at lower clocks for the same time.  float16, heads of 128, 4097 keys: 934
+// TFLOP/s.  float32, heads of 64, 333 keys: 122.  One token of four heads a key
+// head over 16,384 keys: 157 us, 5.1 TB/s.
 constexpr float kSlack = 8.f;
 
 template <class T, int DP, int NR, bool SPLIT>
@@ -43,7 +51,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
         const bool ok = row < a.rows;
         const int64_t off = pair_offset(r, j, a, a.sq) + (ok ? row_offset(row, a, a.sq) : 0);
 #pragma unroll
-        for (int f = 0; f < TL::FR; ++f) 
+        for (int f = 0; f < TL::FR; ++f)
             qf[n][f] = make_frag<T, true>(load_raw<T>(a.q, off, 2 * f + half, a.D, ok));
 #pragma unroll
         for (int d = 0; d < TL::DT; ++d)
