@@ -242,14 +242,14 @@ constexpr int kAttnWaves = kAttnThreads / 64;
 // of the chunk index with bits of the row, so that neither the row reads (32
 // rows, one chunk) nor the transposed reads (4 rows, 4 chunks) of a wavefront
 // fall on the same banks.
-template <class T, int DP>
+template <class T, int DP, int ROWS = T::kPlanes == 3 ? 32 : 64>
 struct Tile {
     static constexpr int kSize = T::kSize;
     static constexpr int EPC = 8;               // values per chunk
     static constexpr int CH = DP / EPC;         // chunks per row
     static constexpr int FR = CH / 2;           // fragments over a row
     static constexpr int ROWB = DP * 2;         // bytes per row
-    static constexpr int BN = T::kPlanes == 3 ? 32 : 64;  // rows per tile
+    static constexpr int BN = ROWS;
     static constexpr int SUB = BN / 32;
     static constexpr int NB = 2;                // contraction blocks of 32 rows
     static constexpr int DT = DP / 32;          // 32-wide column tiles
@@ -361,9 +361,8 @@ __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70
 // head's size) keep what they held: zero, or a value of an earlier tile of the
 // same sequence, which only meets factors of zero.  float32 passes through
 // registers and is split on the way; places that are not loaded become zero.
-template <class T, int DP, bool SCORE>
+template <class T, int DP, bool SCORE, class TL = Tile<T, DP>>
 struct Loader {
-    using TL = Tile<T, DP>;
     static constexpr bool kDirect = T::kPlanes == 1;
     static_assert(!kDirect || TL::kChunks % kAttnThreads == 0, "every lane has a chunk");
     const char *p[TL::NCH];
@@ -474,8 +473,8 @@ __device__ __forceinline__ int64_t row_offset(uint32_t row, const AttnArgs &a, c
     const uint32_t m = div_by(t, a.len_q), i = t - m * a.len_q.d;
     return static_cast<int64_t>(m) * s.b + static_cast<int64_t>(i) * s.t + static_cast<int64_t>(hr) * s.h;
 }
-template <class T, int DP, bool SCORE>
-__device__ __forceinline__ void Loader<T, DP, SCORE>::point_rows(const void *base, int64_t off, const HeadStrides &s,
+template <class T, int DP, bool SCORE, class TL>
+__device__ __forceinline__ void Loader<T, DP, SCORE, TL>::point_rows(const void *base, int64_t off, const HeadStrides &s,
                                                           int64_t row0, const AttnArgs &a) {
 #pragma unroll
     for (int i = 0; i < TL::NCH; ++i)

@@ -217,11 +217,22 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
 // Measured (as above): 350 us over 512 keys, 66 to 75 us for each 128 keys more (900 to
 // 1050 TFLOP/s).  A wavefront waits on LDS for 47% of its time: two of them a
 // SIMD hold all registers (64 sums and 32 of K and V for heads of 64), so
-// reads further ahead have no place.  Heads of 128 (float32: of 96 and more)
-// need the registers of one wavefront a SIMD: at two they would spill.
+// reads further ahead have no place.
+//
+// 16-bit heads of 128: 192 registers of sums, K and V leave too few for two
+// wavefronts a SIMD, and one alone waits (and moves its sums between register
+// files).  K goes to LDS there, each lane its own operands, and tiles have 32
+// rows so that two workgroups fit: 270 -> 180 us for 8 regions of 512 keys, 64
+// maps of 64 tokens, 8 heads.  At 96 it gives nothing (122 for 124 us), and
+// float32 heads of 96 and more find LDS full: they run one wavefront a SIMD.
+constexpr bool dkv_keys_in_lds(int size, int dim) { return size == 2 && dim > 96; }
+constexpr int dkv_tile_rows(int size, int dim) { return size == 4 || dim > 96 ? 32 : 64; }
+
 template <class T, int DP, bool SPLIT>
-__global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 : 1)) void k_attn_dkv(const AttnArgs a, int64_t block0) {
-    using TL = Tile<T, DP>;
+__global__ __launch_bounds__(kAttnThreads, (T::kSize * DP <= 256 ? 2 : 1)) void k_attn_dkv(const AttnArgs a, int64_t block0) {
+    using TL = Tile<T, DP, dkv_tile_rows(T::kSize, DP)>;
+    constexpr bool kKeysInLds = dkv_keys_in_lds(T::kSize, DP);
+    __shared__ __align__(16) u32x4 s_k[kKeysInLds ? kAttnThreads * TL::FR : 1];
     __shared__ __align__(16) char s_qg[2][2 * TL::kBytes];  // Q tile, dO tile; two of each
     __shared__ __align__(16) float s_stat[2][2 * TL::BN];   // lse log2(e), delta of the tile's rows
     const int tid = static_cast<int>(threadIdx.x);
@@ -237,13 +248,17 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
     bool key_ok = key < n_keys;
     if (a.key_mask && key_ok) key_ok = a.key_mask[static_cast<int64_t>(r) * a.Lk + key] != 0;
     const bool idle = !__any(key_ok);  // no key of this wavefront is attended
-    Frag<T> kf[TL::FR], vf[TL::FR];
+    Frag<T> kf[kKeysInLds ? 1 : TL::FR], vf[TL::FR];
     {
         const int64_t offk = static_cast<int64_t>(r) * a.sk.b + static_cast<int64_t>(j) * a.sk.h + (key_ok ? key * a.sk.t : 0);
         const int64_t offv = static_cast<int64_t>(r) * a.sv.b + static_cast<int64_t>(j) * a.sv.h + (key_ok ? key * a.sv.t : 0);
 #pragma unroll
         for (int f = 0; f < TL::FR; ++f) {
-            kf[f] = make_frag<T, true>(load_raw<T>(a.k, offk, 2 * f + half, a.D, key_ok));
+            const Frag<T> x = make_frag<T, true>(load_raw<T>(a.k, offk, 2 * f + half, a.D, key_ok));
+            if constexpr (kKeysInLds)
+                s_k[f * kAttnThreads + tid] = x.p[0];  // read by the same lane only
+            else
+                kf[f] = x;
             vf[f] = make_frag<T, false>(load_raw<T>(a.v, offv, 2 * f + half, a.D, key_ok));
         }
     }
@@ -260,8 +275,8 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
     const float *delta = a.delta + static_cast<int64_t>(pair) * a.rows;
 
     constexpr uint64_t kAll = ~0ull >> (64 - TL::BN);
-    Loader<T, DP, true> gq;
-    Loader<T, DP, false> gg;
+    Loader<T, DP, true, TL> gq;
+    Loader<T, DP, false, TL> gg;
     float g_lse = 0.f, g_delta = 0.f;
     // With whole groups of rep rows in a tile and the maps in one run, a tile's
     // rows lie a constant step after the last tile's.
@@ -323,7 +338,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
         for (int t = 0; t < TL::SUB; ++t) {
             if (idle) break;
             // Reads of LDS spread between the products: 679 -> 651 us for the 2048-map training batch (forward included).
-            if constexpr (T::kPlanes == 1 && DP <= 64) __builtin_amdgcn_iglp_opt(0);
+            if constexpr (T::kPlanes == 1 && (DP <= 64 || kKeysInLds)) __builtin_amdgcn_iglp_opt(0);
             f32x16 s, g;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = 0.f;
@@ -335,7 +350,8 @@ __global__ __launch_bounds__(kAttnThreads, (DP <= (T::kSize == 4 ? 64 : 96) ? 2 
             }
 #pragma unroll
             for (int f = 0; f < TL::FR; ++f) {
-                s = mma<T>(TL::frag(s_q, t * 32 + col, f, half), kf[f], s);
+                if constexpr (kKeysInLds) kf[0].p[0] = s_k[f * kAttnThreads + tid];
+                s = mma<T>(TL::frag(s_q, t * 32 + col, f, half), kf[kKeysInLds ? 0 : f], s);
                 g = mma<T>(TL::frag(s_g, t * 32 + col, f, half), vf[f], g);
             }
 #pragma unroll
@@ -431,11 +447,12 @@ struct BwdPlan {
 };
 BwdPlan bwd_plan(const AttnArgs &a, int32_t dtype) {
     const int64_t bn = dtype == kF32 ? 32 : 64;
+    const int64_t bk = dkv_tile_rows(dtype == kF32 ? 4 : 2, a.D);
     BwdPlan p;
     p.pairs = static_cast<int64_t>(a.n_kv) * a.Hk;
     p.nr = attn_row_blocks(a, dtype);
     p.q = attn_plan(p.pairs, (static_cast<int64_t>(a.rows) + 128 * p.nr - 1) / (128 * p.nr), (a.Lk + bn - 1) / bn, kSplitLeast / bn);
-    p.kv = attn_plan(p.pairs, (static_cast<int64_t>(a.Lk) + 127) / 128, (a.rows + bn - 1) / bn, kSplitLeast / bn);
+    p.kv = attn_plan(p.pairs, (static_cast<int64_t>(a.Lk) + 127) / 128, (a.rows + bk - 1) / bk, kSplitLeast / bk);
     p.bytes_delta = round16(p.pairs * a.rows * 4);
     p.bytes_q = p.q.n_split > 1 ? p.q.n_split * p.pairs * a.rows * a.D * 4 : 0;
     p.bytes_kv = p.kv.n_split > 1 ? 2 * p.kv.n_split * p.pairs * a.Lk * a.D * 4 : 0;
