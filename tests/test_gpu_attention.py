@@ -134,6 +134,30 @@ def test_split_with_empty_parts():
     check_case(c)
 
 
+@pytest.mark.parametrize("dtype,dim", [("float32", 40), ("bfloat16", 40), ("bfloat16", 128)])
+@pytest.mark.parametrize("len_k", [600, 1300, 9000])
+def test_two_to_dozens_of_parts(dtype, dim, len_k):
+    """Every way the parts of a row are shared out: all attended, two keys far apart, one key, none."""
+    torch, dev = torch_dev()
+    say(f"attention, {dtype}, heads of {dim}, {len_k} keys in parts")
+    c = make(dtype, 4, 1, 3, len_k, 3, 1, dim, "none", seed=len_k)
+    m = torch.zeros(4, len_k, dtype=torch.uint8)
+    m[0] = 1
+    m[1, 7] = m[1, len_k - 2] = 1
+    m[2, len_k // 2] = 1
+    c["key_mask"] = m.to(dev)
+    check_case(c)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("group,len_q,heads,heads_kv,len_k", [
+    (1, 1, 1, 1, 129), (1, 33, 2, 1, 128), (2, 31, 6, 2, 200), (9, 64, 4, 4, 70), (5, 7, 5, 1, 300)])
+def test_rows_of_wide_heads(dtype, group, len_q, heads, heads_kv, len_k):
+    for dim in (96, 120, 128):
+        say(f"attention, {dtype}, heads of {dim}, group {group}, {len_q} tokens, heads {heads}/{heads_kv}, {len_k} keys")
+        check_case(make(dtype, 2, group, len_q, len_k, heads, heads_kv, dim, "both", seed=len_k))
+
+
 def test_lengths_outside_their_range_are_taken_in():
     torch, dev = torch_dev()
     c = make("float32", 3, 2, 5, 40, 2, 2, 32, "none")
@@ -364,4 +388,16 @@ def test_binding_refuses():
     ]
     for f in refused:
         with pytest.raises(pc.PCError):
+            f()
+
+
+def test_binding_names_a_missing_tensor():
+    torch, dev = torch_dev()
+    say("attention, a tensor that is None")
+    c = make("bfloat16", 2, 2, 5, 40, 4, 2, 64, "none")
+    q, k, v = c["q"], c["k"], c["v"]
+    lse = torch.empty(4, 5, 4, device=dev)
+    for f, name in ((lambda: pc.pc_cross_attention(q, k, v, None), "out"),
+                    (lambda: pc.pc_cross_attention_backward(q, k, v, q.clone(), lse, None, q.clone(), k.clone(), v.clone()), "dout")):
+        with pytest.raises(ValueError, match=f"^{name} is required"):
             f()

@@ -246,6 +246,8 @@ def _dtype(t, name: str) -> int:
 
 def _like(t, name: str, shape, ref):
     """(address, strides) of a [batch, len, heads, dim] tensor on ref's device and of its type, heads contiguous."""
+    if t is None:
+        raise ValueError(f"{name} is required")
     stride = t.stride()
     if t.device != ref.device or t.dtype != ref.dtype or t.shape != shape or stride[3] != 1:
         raise ValueError(f"{name} must be {ref.dtype} of shape {tuple(shape)} on {ref.device} with the values of a head "

@@ -26,7 +26,7 @@ namespace {
 // units 73% and the matrix units 39% busy; forms with fewer instructions ran
 // at lower clocks for the same time.  float16, heads of 128, 4097 keys: 934
 // TFLOP/s.  float32, heads of 64, 333 keys: 122.  One token of four heads a key
-// head over 16,384 keys: 157 us, 5.1 TB/s.
+// head over 16,384 keys: 155 us, 5.2 TB/s.
 constexpr float kSlack = 8.f;
 
 template <class T, int DP, int NR, bool SPLIT>
@@ -224,38 +224,69 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
     }
 }
 
-// Joins the splits of a row: lane (row, 4 columns) weighs each split's partial
-// sum by 2^((m_s - m) c), in split order.
-__global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, int32_t dtype, int64_t total, int64_t block0) {
-    const int64_t id = (block0 + blockIdx.x) * 256 + threadIdx.x;
-    if (id >= total) return;
+// Joins the splits of a row.  256 lanes of a workgroup hold (row, 4 columns)
+// each; SETS such sets of lanes share the splits (set g those with s % SETS =
+// g, in order), and the sets are joined in order: a row of one token may have
+// hundreds of splits, and one lane's reads of them would wait on each other
+// (one token of 32 heads over 65,536 keys, 8 key heads of 128, 64 splits: 55 us
+// a lane alone, 8.4 in four sets).  Below 256 workgroups there are four; with
+// rows enough to fill the card one set reads best (16 x 128 rows of 8 heads of
+// 128, 4 splits: 8.1 us; shared, 14.6).
+template <int SETS>
+__global__ __launch_bounds__(256 * SETS) void k_attn_join(const AttnArgs a, int32_t dtype, int64_t total, int64_t block0) {
+    __shared__ float s_m[SETS][SETS > 1 ? 256 : 1], s_l[SETS][SETS > 1 ? 256 : 1];
+    __shared__ __align__(16) f32v4 s_o[SETS][SETS > 1 ? 256 : 1];
+    const uint32_t at = threadIdx.x & 255, g = threadIdx.x >> 8;
+    const int64_t id = (block0 + blockIdx.x) * 256 + at;
+    const bool ok = id < total;
     const uint32_t quads = a.D / 4;
     const int64_t slot0 = id / quads;  // pair * rows + row
     const int d = static_cast<int>(id - slot0 * quads) * 4;
+    const int64_t step = static_cast<int64_t>(a.n_kv) * a.Hk * a.rows;
+    // Without branches, several splits' loads in flight.  A split without an
+    // attended key has m = -inf, l = -1 and zeros.
+    float m = -INFINITY, l = 0.f;
+    bool seen = false;
+    f32v4 o = {0.f, 0.f, 0.f, 0.f};
+    if (ok) {
+#pragma unroll 4
+        for (uint32_t s = g; s < a.n_split.d; s += SETS) {
+            seen |= a.part_ml[2 * (slot0 + s * step) + 1] != -1.f;
+            m = fmaxf(m, a.part_ml[2 * (slot0 + s * step)]);
+        }
+        const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
+#pragma unroll 4
+        for (uint32_t s = g; s < a.n_split.d; s += SETS) {
+            const int64_t slot = slot0 + s * step;
+            const float ms = a.part_ml[2 * slot], ls = a.part_ml[2 * slot + 1];
+            const f32v4 x = *reinterpret_cast<const f32v4 *>(a.part + slot * a.D + d);
+            const float w = exp2_hw(fmaf(ms, a.scale_log2, -base));
+            l = fmaf(ls == -1.f ? 0.f : ls, w, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = fmaf(x[i], w, o[i]);
+        }
+    }
+    if constexpr (SETS > 1) {
+        s_o[g][at] = o;
+        s_m[g][at] = m;
+        s_l[g][at] = seen ? l : -1.f;
+        __syncthreads();
+        if (g != 0) return;
+        for (int k = 1; k < SETS; ++k) m = fmaxf(m, s_m[k][at]);
+        const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
+        l = 0.f;
+        o = f32v4{0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < SETS; ++k) {
+            const float lk = s_l[k][at], w = exp2_hw(fmaf(s_m[k][at], a.scale_log2, -base));
+            seen |= lk != -1.f;
+            l = fmaf(lk == -1.f ? 0.f : lk, w, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = fmaf(s_o[k][at][i], w, o[i]);
+        }
+    }
+    if (!ok) return;
     const uint32_t pair = static_cast<uint32_t>(slot0 / a.rows), row = static_cast<uint32_t>(slot0 - static_cast<int64_t>(pair) * a.rows);
     const uint32_t r = pair / a.Hk, j = pair - r * a.Hk;
-    const int64_t step = static_cast<int64_t>(a.n_kv) * a.Hk * a.rows;
-    float m = -INFINITY;
-    bool seen = false;
-    for (uint32_t s = 0; s < a.n_split.d; ++s) {
-        const float ls = a.part_ml[2 * (slot0 + s * step) + 1];
-        if (ls == -1.f) continue;
-        seen = true;
-        m = fmaxf(m, a.part_ml[2 * (slot0 + s * step)]);
-    }
-    const float base = m == -INFINITY ? 0.f : m * a.scale_log2;
-    float l = 0.f;
-    f32v4 o = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t s = 0; s < a.n_split.d; ++s) {
-        const int64_t slot = slot0 + s * step;
-        const float ls = a.part_ml[2 * slot + 1];
-        if (ls == -1.f) continue;
-        const float w = exp2_hw(fmaf(a.part_ml[2 * slot], a.scale_log2, -base));
-        l = fmaf(ls, w, l);
-        const f32v4 x = *reinterpret_cast<const f32v4 *>(a.part + slot * a.D + d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = fmaf(x[i], w, o[i]);
-    }
     const float inv = seen ? 1.f / l : 0.f;
     const int64_t off = pair_offset(r, j, a, a.so) + row_offset(row, a, a.so) + d;
     if (dtype == kBf16)
@@ -308,9 +339,13 @@ hipError_t launch_attn_fwd(AttnArgs a, int32_t dtype, char *workspace, hipStream
         });
     });
     if (e != hipSuccess || p.n_split == 1) return e;
-    const int64_t total = pairs * a.rows * (a.D / 4);
-    return launch_slices((total + 255) / 256, 256, [&](int64_t first, uint32_t count) {
-        k_attn_join<<<count, 256, 0, stream>>>(a, dtype, total, first);
+    const int64_t total = pairs * a.rows * (a.D / 4), wgs = (total + 255) / 256;
+    if (wgs < 256 && p.n_split > 2)
+        return launch_slices(wgs, 1024, [&](int64_t first, uint32_t count) {
+            k_attn_join<4><<<count, 1024, 0, stream>>>(a, dtype, total, first);
+        });
+    return launch_slices(wgs, 256, [&](int64_t first, uint32_t count) {
+        k_attn_join<1><<<count, 256, 0, stream>>>(a, dtype, total, first);
     });
 }
 
