@@ -125,6 +125,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 384 ? 2 : 1)) void k
                 for (int i = 0; i < 16; ++i) s[n][i] = g[n][i] = 0.f;
 #pragma unroll
             for (int f = 0; f < TL::FR; ++f) {
+                if (TL::past(f, a.D)) continue;
                 const Frag<T> kf = TL::frag(s_k, t * 32 + col, f, half), vf = TL::frag(s_v, t * 32 + col, f, half);
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
@@ -350,6 +351,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP <= 256 ? 2 : 1)) void 
             }
 #pragma unroll
             for (int f = 0; f < TL::FR; ++f) {
+                if (TL::past(f, a.D)) continue;
                 if constexpr (kKeysInLds) kf[0].p[0] = s_k[f * kAttnThreads + tid];
                 s = mma<T>(TL::frag(s_q, t * 32 + col, f, half), kf[kKeysInLds ? 0 : f], s);
                 g = mma<T>(TL::frag(s_g, t * 32 + col, f, half), vf[f], g);

@@ -112,6 +112,7 @@ __global__ __launch_bounds__(kAttnThreads, (T::kSize * DP < 512 ? 2 : 1)) void k
                     for (int i = 0; i < 16; ++i) s[n][t][i] = 0.f;
 #pragma unroll
                 for (int f = 0; f < TL::FR; ++f) {
+                    if (TL::past(f, a.D)) continue;
                     const Frag<T> kf = TL::frag(s_k, t * 32 + col, f, half);
 #pragma unroll
                     for (int n = 0; n < NR; ++n) s[n][t] = mma<T>(kf, qf[n][f], s[n][t]);
